@@ -46,7 +46,8 @@
  * sgd_workspace_status after the stream completes.  No call aborts, traps or
  * throws.
  * Limits.  1 <= G <= 16 (query heads per KV head); D in {64, 128}; Hkv * T < 2^31; B >= 1,
- * Hkv >= 1; several query tokens: G * M <= 64 for the decode, <= 16 for the selection.
+ * Hkv >= 1; several query tokens: G * M <= 64 for the decode, <= 16 for the selection, M <= 64
+ * (and any G <= 16) for the paged attention.
  */
 #ifndef SGD_H_
 #define SGD_H_
@@ -103,6 +104,9 @@ typedef enum {
 #define SGD_STATUS_SIZE_MISMATCH 0x4  /* device lengths disagree with host sizes */
 #define SGD_STATUS_BAD_INDEX 0x8      /* a kept index or block number was outside its sequence */
 #define SGD_STATUS_BAD_SCALE 0x10     /* a calibrated scale was negative or not finite: its codes are 0 */
+#define SGD_STATUS_NO_PAGES 0x20      /* the pool has too few free pages: the call changed nothing */
+#define SGD_STATUS_SHARED_PAGE 0x40   /* a page that another row holds too would have been written */
+#define SGD_STATUS_BAD_PROBS 0x80     /* a distribution to sample from had no positive entry */
 
 #define SGD_WS_STATUS_OFFSET 0
 
@@ -381,6 +385,173 @@ int sgd_decode_attn_noalloc(const void *q, sgd_dtype q_dtype, int G, const sgd_k
                             const int32_t *idx, const int32_t *cu_kept, int64_t kept_total,
                             int schedule, int n_splits, int q_quant, float *out, float *lse, int32_t *status,
                             void *stream);
+
+/* ------------------------------------------------------------------------------------------
+ * The paged cache: sequences whose K and V live in 64-token pages of one pool, so that a
+ * sequence grows, forks, shrinks and ends without moving another.  The calls below are the
+ * serving loop around it: pages_reserve and pages_append write a step's tokens, paged_attn
+ * attends over them (one token, a chain or a tree of drafted tokens, a sliding window),
+ * verify_tree accepts drafted tokens, pages_accept keeps the accepted ones, pages_fork,
+ * pages_keep and pages_release branch, cut and end sequences.  All state is in device memory
+ * and every call is stream-ordered, so a whole step runs, and is captured, without the host.
+ * The pages have no counterpart to these entry points ([CD] names speculative decoding, [NSA]
+ * section 2.1 reads the cache by 64-token blocks).
+ *
+ * Sequence b (a row of the page table) holds lens[b] tokens; its token t is slot t % 64 of page
+ * page_table[b * max_pages + t / 64].  A page belongs to every row that lists it among its first
+ * held[b] entries; ref_count[p] counts them, and 0 means free.  Slots behind the last token
+ * may hold anything, NaN included, and are left as they are.
+ * ------------------------------------------------------------------------------------------ */
+#define SGD_PAGE 64       /* tokens of a page */
+#define SGD_MAX_NODES 64  /* query tokens of a sequence in one step of the paged calls */
+
+typedef struct {
+    sgd_dtype dtype;          /* of k and v: BF16, or I8 (codes with per-tensor scales) */
+    int32_t B;                /* rows of the page table */
+    int32_t Hkv;              /* KV heads */
+    int32_t D;                /* head dim, 64 or 128 */
+    int32_t n_pages;          /* pages of the pool; n_pages * Hkv * 64 < 2^31 */
+    int32_t max_pages;        /* entries of a page table row */
+    void *k;                  /* [n_pages, Hkv, 64, D] */
+    void *v;                  /* [n_pages, Hkv, 64, D] */
+    const float *k_scale;     /* I8: [1], the calibrated per-tensor scales of scheme B */
+    const float *v_scale;     /* I8: [1] */
+    int32_t *page_table;      /* [B, max_pages] */
+    int32_t *lens;            /* [B] */
+    int32_t *held;            /* [B]; read by _reserve, _fork and _release (may be NULL for the others) */
+    int32_t *ref_count;       /* [n_pages]; may be NULL for sgd_paged_attn and sgd_pages_append */
+} sgd_paged_kv;
+
+/* Workspace bytes of every call that takes an sgd_paged_kv, with up to M query tokens and G query
+ * heads per KV head.  Returns 0 on invalid arguments. */
+size_t sgd_paged_workspace_size(const sgd_paged_kv *kv, int G, int M);
+
+/*
+ * sgd_paged_attn -- attention of a step's M query tokens per sequence over the paged cache.
+ *   The step's n = n_nodes[b] real nodes (M where n_nodes is NULL) are the cache's last n
+ *   entries: node m is cache entry base + m, base = lens[b] - n.  parent[b, m] is the node before
+ *   it, -1 for a root, and always smaller than m; parent == NULL is the chain (node m follows
+ *   m - 1).  depth(m) counts the steps up to its root; its position in the text is
+ *   base + depth(m).  Query m attends to the cached entries t < base, to itself and to its
+ *   ancestors; with a window > 0 only to those of them at a position above
+ *   position(m) - window (itself and the window - 1 positions before) or below `sinks`.
+ *   out[b, m, h] = sum_t softmax_t(z_t) vhat_t, z_t = q[b, m, h] . khat_t / sqrt(D);
+ *   lse[b, m, h] = ln sum_t exp(z_t).  A query that sees nothing (m >= n_nodes[b], an entry
+ *   before the cache's first) gets out = 0 and lse = -inf.
+ * q        [B, M, Hq, D] BF16, Hq = Hkv * G, 1 <= G <= 16, 1 <= M <= SGD_MAX_NODES
+ * parent   [B, M] int32 or NULL; n_nodes [B] int32 or NULL
+ * window   >= 0, 0 = unlimited; sinks >= 0, read with a window only
+ * out      [B, M, Hq, D] BF16; lse [B, M, Hq] float32, natural log
+ * K and V of an entry that no query of the sequence sees may be anything; those of an entry that
+ * some query sees must be finite.
+ * Status: BAD_INDEX for a page outside the pool (page 0 is read), a parent outside [-1, m) (taken
+ * as -1) or n_nodes outside [0, M] (clamped); SIZE_MISMATCH for lens[b] outside
+ * [0, 64 * max_pages] (clamped); BAD_SCALE as in sgd_quantize_kv.
+ */
+int sgd_paged_attn(const void *q, int G, int M, const sgd_paged_kv *kv, const int32_t *parent,
+                   const int32_t *n_nodes, int window, int sinks, void *out, float *lse, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/*
+ * sgd_verify_tree -- drafted tokens against the target's distributions, from given random numbers.
+ *   Node 0 is the last accepted token, the other nodes are drafted tokens (tokens, parent as in
+ *   sgd_paged_attn).  p[b, m] is the target's distribution after node m, q[b, m] the one that
+ *   the children of node m were drawn from, independently of each other.  The walk stands at node 0
+ *   with w = p[b, 0], Z = 1.  It tests the children of its node in the order of their numbers:
+ *   child c with token x is accepted if u_accept[b, c] * q(x) * Z < w(x), and the walk goes on
+ *   from c with w = p[b, c], Z = 1; otherwise w becomes max(w / Z - q, 0), Z its sum (kept as
+ *   they were where that sum is not positive).  q == NULL: the drafts were not drawn but chosen;
+ *   q(x) is 1 in the test and a refused token's w(x) becomes 0.  Where no child is left the next
+ *   token is drawn from w: the lowest x with w(0) + .. + w(x) > u_sample[b] * sum w.
+ *   Products, sums and residuals are formed in 64 bits.
+ * p, q     [B, M, V], F32 or BF16 (p_dtype, for both)
+ * tokens   [B, M] int32 (node 0's is not read); parent [B, M] int32; n_nodes [B] int32 or NULL
+ * u_accept [B, M] float32; u_sample [B] float32, in [0, 1)
+ * n_path   [B] int32: nodes of the accepted path, node 0 among them
+ * path     [B, M] int32: its nodes in order, then -1
+ * next_token [B] int32.  A sequence without nodes gets n_path 0 and next_token -1.
+ * Status: BAD_INDEX for a drafted token outside [0, V), a parent outside [-1, m) (neither is ever
+ * accepted) or n_nodes outside [0, M] (clamped); BAD_PROBS where w has no positive entry
+ * (next_token 0).
+ * workspace   at least 256 bytes
+ */
+int sgd_verify_tree(const void *p, sgd_dtype p_dtype, const void *q, int B, int M, int64_t V, const int32_t *tokens,
+                    const int32_t *parent, const int32_t *n_nodes, const float *u_accept, const float *u_sample,
+                    int32_t *n_path, int32_t *path, int32_t *next_token, void *workspace, size_t workspace_bytes,
+                    void *stream);
+
+/*
+ * sgd_pages_reserve -- room for add[b] more tokens of each row: the pages that lens[b] + add[b]
+ * tokens need beyond held[b] are taken from the free ones, lowest page first, rows in order, and
+ * entered in the page table; held and ref_count follow.  new_lens[b] = lens[b] + add[b] (lens
+ * itself stays: pass new_lens as the next calls' lens).
+ * The call changes nothing (new_lens = lens) and sets NO_PAGES where the free pages do not
+ * suffice, SIZE_MISMATCH where a row would pass max_pages or add, lens or held is out of range,
+ * SHARED_PAGE where a row would grow inside a page that another row holds too, BAD_INDEX where
+ * the page it would grow in is outside the pool.
+ * add      [B] int32, >= 0;  new_lens [B] int32 (may be lens itself)
+ */
+int sgd_pages_reserve(const sgd_paged_kv *kv, const int32_t *add, int32_t *new_lens, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/*
+ * sgd_pages_append -- K and V of new tokens into the pages: of row b the tokens
+ * cu_new[b] .. cu_new[b+1] - 1 of k_new and v_new become its last cu_new[b+1] - cu_new[b] entries
+ * (lens[b] counts them already, as after sgd_pages_reserve).  An I8 cache takes their codes under
+ * its scales, as sgd_quantize_kv with SGD_SCHEME_B_CALIBRATED makes them.
+ * k_new, v_new   [Hkv, T_new, D] BF16;  cu_new [B+1] int32, T_new = cu_new[B] (host value)
+ * Status: BAD_INDEX for a page outside the pool, SIZE_MISMATCH for a token outside the row or a
+ * cu_new that disagrees with T_new (those tokens are not written); BAD_SCALE.
+ */
+int sgd_pages_append(const sgd_paged_kv *kv, const void *k_new, const void *v_new, const int32_t *cu_new,
+                     int64_t T_new, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * sgd_pages_fork -- row dst[i] becomes a copy of row src[i], i < n: full pages are shared
+ * (ref_count + 1), the tokens of a part-filled last page are copied into a free page, lowest page
+ * first in the order of i; page table, lens, held and ref_count of the new rows follow.
+ * src, dst [n] int32 row numbers; every dst once, none of them a src, with held[dst] = 0
+ * The call changes nothing and sets NO_PAGES where the free pages do not suffice, BAD_INDEX for
+ * rows against those rules or a part-filled page outside the pool, SIZE_MISMATCH for a src whose
+ * lens, held and max_pages disagree.  A full page outside the pool sets BAD_INDEX and is entered
+ * as it is.
+ */
+int sgd_pages_fork(const sgd_paged_kv *kv, const int32_t *src, const int32_t *dst, int n, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/*
+ * sgd_pages_release -- every row b gives back the pages behind its first keep[b] tokens: entries
+ * ceil(keep[b] / 64) .. held[b] - 1 of its page table lose a reference, held[b] shrinks.  keep 0
+ * ends a row, keep = lens[b] returns what was reserved and not used.  lens is not touched.
+ * keep     [B] int32, >= 0
+ * Status: BAD_INDEX for a page outside the pool or without references (skipped), SIZE_MISMATCH
+ * for a negative keep (taken as 0) or held[b] outside [0, max_pages] (clamped).
+ */
+int sgd_pages_release(const sgd_paged_kv *kv, const int32_t *keep, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
+/*
+ * sgd_pages_accept -- of a step's n_nodes[b] nodes (the last entries of row b) the accepted ones
+ * stay: entry base + path[b, i] moves to base + i, i < n_path[b], base = lens[b] - n_nodes[b];
+ * new_lens[b] = base + n_path[b].  path and n_path as written by sgd_verify_tree (ascending).
+ * path     [B, M] int32; n_path, n_nodes [B] int32; new_lens [B] int32, not lens itself
+ * Status: BAD_INDEX for a path that does not ascend or leaves the nodes (clamped) or a page outside
+ * the pool, SIZE_MISMATCH for counts out of range (clamped), SHARED_PAGE for a row that would
+ * write a shared page (left as it is, new_lens = lens).
+ */
+int sgd_pages_accept(const sgd_paged_kv *kv, const int32_t *path, const int32_t *n_path, const int32_t *n_nodes,
+                     int M, int32_t *new_lens, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * sgd_pages_keep -- token dropping made permanent: of row b and KV head h the tokens
+ * idx[h, cu_kept[b] .. cu_kept[b+1] - 1] (ascending, as sgd_oam_select writes them) become its
+ * first ones, in order; new_lens[b] = cu_kept[b+1] - cu_kept[b].  A row with none keeps none.
+ * idx      [Hkv, kept_total] int32; cu_kept [B+1] int32; new_lens [B] int32, not lens itself
+ * Status as in sgd_pages_accept.  The pages that fell empty are given back by
+ * sgd_pages_release(kv, new_lens, ...).
+ */
+int sgd_pages_keep(const sgd_paged_kv *kv, const int32_t *idx, const int32_t *cu_kept, int64_t kept_total,
+                   int32_t *new_lens, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Copies the device status word of `workspace` to *status (host) after
  * synchronising `stream`.  The only call that synchronises. */

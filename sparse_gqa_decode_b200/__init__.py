@@ -18,6 +18,19 @@ Variants: ``oam_select`` on a bf16/f32 cache or on the INT8 cache with stored va
 ``decode_attn(..., q_quant="token"|"tensor")`` for INT8 query codes; ``oam_select_multi`` /
 ``decode_attn_multi`` for several query tokens per sequence (speculative decoding);
 ``oam_select_blocks`` / ``decode_attn_blocks`` for whole 64-token blocks.
+
+A speculative step over a paged cache (``PagedKv``; all state stays on the device)::
+
+    grown, _ = pages_reserve(cache, n_nodes)              # room for the step's nodes
+    step = cache.with_lens(grown)
+    pages_append(step, k_new, v_new, cu_new)              # their keys and values
+    out, lse, _ = paged_attn(q, G, step, parent=parent, n_nodes=n_nodes, window=0, sinks=0)
+    n_path, path, token, _ = verify_tree(p, tokens, parent, u_accept, u_sample, q=draft_p, n_nodes=n_nodes)
+    lens, _ = pages_accept(step, path, n_path, n_nodes)   # the accepted nodes stay
+    cache = cache.with_lens(lens)
+
+``pages_fork`` branches a sequence, ``pages_keep`` cuts it to selected tokens (as ``oam_select``
+returns them), ``pages_release`` gives pages back.
 """
 from __future__ import annotations
 
@@ -33,7 +46,9 @@ __all__ = [
     "decode_attn_multi", "decode_attn_blocks", "decode_attn_noalloc", "plan_segments", "workspace_status",
     "workspace_size", "decode_num_ctas", "kept_total", "kept_blocks_total", "n_parts", "kernel_timing_start",
     "kernel_timing_stop", "test_pipeline_timeout", "stream_read", "gather_read", "SGD_F32", "SGD_BF16", "SGD_I8", "SCHEME_A", "SCHEME_B",
-    "SCHEME_A_CALIBRATED", "SCHEME_B_CALIBRATED", "STATUS_BITS", "ROW_COST",
+    "SCHEME_A_CALIBRATED", "SCHEME_B_CALIBRATED", "STATUS_BITS", "ROW_COST", "PAGE", "MAX_NODES", "PagedKv",
+    "paged_workspace_size", "paged_attn", "verify_tree", "pages_reserve", "pages_append", "pages_fork",
+    "pages_release", "pages_accept", "pages_keep",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -45,7 +60,10 @@ ROW_COST = 512  # SGD_ROW_COST: the automatic split's work charge per row, in to
 OP_QUANTIZE, OP_OAM_SELECT, OP_DECODE, OP_QUANTIZE_SELECT = 0, 1, 2, 3
 PARTITION = 64
 STATUS_BITS = {0x1: "empty sequence", 0x2: "wait timeout", 0x4: "size mismatch", 0x8: "bad index",
-               0x10: "bad calibrated scale"}
+               0x10: "bad calibrated scale", 0x20: "too few free pages", 0x40: "shared page",
+               0x80: "no positive probability"}
+PAGE = 64  # SGD_PAGE: tokens of a page of the paged cache
+MAX_NODES = 64  # SGD_MAX_NODES: query tokens of a sequence in one step of the paged calls
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python sparse_gqa_decode_b200/build.py` "
@@ -107,6 +125,38 @@ lib.sgd_quantize_select_blocks.argtypes = [_vp, _i32, _i32, _kvp, _f, _f, _i32, 
                                            _vp, _vp, _i64, _vp, _vp, _i64, _vp, _sz, _vp]
 lib.sgd_decode_attn_noalloc.argtypes = [_vp, _i32, _i32, _kvp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp,
                                         _vp]
+
+
+class _PagedKvStruct(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int),
+        ("B", ctypes.c_int32),
+        ("Hkv", ctypes.c_int32),
+        ("D", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("lens", ctypes.c_void_p),
+        ("held", ctypes.c_void_p),
+        ("ref_count", ctypes.c_void_p),
+    ]
+
+
+_pkvp = ctypes.POINTER(_PagedKvStruct)
+lib.sgd_paged_workspace_size.argtypes = [_pkvp, _i32, _i32]
+lib.sgd_paged_workspace_size.restype = _sz
+lib.sgd_paged_attn.argtypes = [_vp, _i32, _i32, _pkvp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _sz, _vp]
+lib.sgd_verify_tree.argtypes = [_vp, _i32, _vp, _i32, _i32, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+lib.sgd_pages_reserve.argtypes = [_pkvp, _vp, _vp, _vp, _sz, _vp]
+lib.sgd_pages_append.argtypes = [_pkvp, _vp, _vp, _vp, _i64, _vp, _sz, _vp]
+lib.sgd_pages_fork.argtypes = [_pkvp, _vp, _vp, _i32, _vp, _sz, _vp]
+lib.sgd_pages_release.argtypes = [_pkvp, _vp, _vp, _sz, _vp]
+lib.sgd_pages_accept.argtypes = [_pkvp, _vp, _vp, _vp, _i32, _vp, _vp, _sz, _vp]
+lib.sgd_pages_keep.argtypes = [_pkvp, _vp, _vp, _i64, _vp, _vp, _sz, _vp]
 
 _DT = {torch.float32: SGD_F32, torch.bfloat16: SGD_BF16, torch.int8: SGD_I8}
 _QQ = {"none": 0, "token": 1, "tensor": 2}
@@ -529,3 +579,242 @@ def plan_segments(cu: torch.Tensor, B: int, Hkv: int, n_req: int, min_chunk: int
                                  _ptr(ws), ws.numel(), _stream(stream)), "sgd_plan_segments")
     n, ncta = (int(x) for x in nseg.tolist())
     return segs[:n].cpu(), ncta
+
+
+# ------------------------------------------------------------------------------------------
+# the paged cache
+# ------------------------------------------------------------------------------------------
+def _want(t, name: str, dtype, shape, device):
+    """Raises ValueError unless ``t`` is a contiguous tensor of this dtype and shape on ``device``."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}" + ("" if t.is_contiguous() else ", strided"))
+
+
+class PagedKv:
+    """A paged KV cache: the pool ``k``, ``v`` [n_pages, Hkv, 64, D] (bfloat16, or int8 codes under the
+    per-tensor ``k_scale``, ``v_scale`` float32 [1]), ``page_table`` int32 [B, max_pages], ``lens`` int32
+    [B], and for the upkeep calls ``held`` int32 [B] and ``ref_count`` int32 [n_pages].  The tensors stay
+    the caller's; the object only checks them once and holds their addresses."""
+
+    def __init__(self, k, v, page_table, lens, held=None, ref_count=None, k_scale=None, v_scale=None):
+        if k.dim() != 4 or k.shape[2] != PAGE:
+            raise ValueError("k must be [n_pages, Hkv, 64, D]")
+        if k.dtype not in (torch.bfloat16, torch.int8):
+            raise ValueError(f"unsupported cache dtype {k.dtype}")
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be [B, max_pages]")
+        if (k.dtype == torch.int8) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+            raise ValueError("an int8 cache, and no other, has k_scale and v_scale")
+        B, dev, i32 = page_table.shape[0], k.device, torch.int32
+        _want(k, "k", k.dtype, k.shape, dev)
+        _want(v, "v", k.dtype, k.shape, dev)
+        _want(page_table, "page_table", i32, page_table.shape, dev)
+        _want(lens, "lens", i32, (B,), dev)
+        for t, name, dt, n in ((held, "held", i32, B), (ref_count, "ref_count", i32, k.shape[0]),
+                               (k_scale, "k_scale", torch.float32, 1), (v_scale, "v_scale", torch.float32, 1)):
+            if t is not None:
+                _want(t, name, dt, (n,), dev)
+        self.k, self.v, self.page_table, self.lens = k, v, page_table, lens
+        self.held, self.ref_count, self.k_scale, self.v_scale = held, ref_count, k_scale, v_scale
+        self.device, self.B, self.Hkv, self.D = dev, B, k.shape[1], k.shape[3]
+        address = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self._struct = _PagedKvStruct(_DT[k.dtype], B, self.Hkv, self.D, k.shape[0], page_table.shape[1], k.data_ptr(),
+                                      v.data_ptr(), address(k_scale), address(v_scale), page_table.data_ptr(),
+                                      lens.data_ptr(), address(held), address(ref_count))
+        self._ref = ctypes.byref(self._struct)
+
+    def with_lens(self, lens: torch.Tensor) -> "PagedKv":
+        """The same cache with other lengths (as pages_reserve, pages_accept and pages_keep return them)."""
+        return PagedKv(self.k, self.v, self.page_table, lens, self.held, self.ref_count, self.k_scale, self.v_scale)
+
+
+def paged_workspace_size(cache: PagedKv, G: int = 1, M: int = 1) -> int:
+    """Bytes of a workspace for any paged call with up to ``M`` query tokens and ``G`` heads per KV head."""
+    n = lib.sgd_paged_workspace_size(cache._ref, G, M)
+    if n == 0:
+        raise SgdError("sgd_paged_workspace_size rejected the arguments")
+    return int(n)
+
+
+class _On:
+    """The raw stream of a call, and new tensors that belong to it: a tensor made for a call on another
+    stream than the current one is allocated on that stream, so that its memory is not handed on while
+    the call may still run."""
+
+    def __init__(self, device, stream):
+        if device.type == "cuda" and device.index != torch.cuda.current_device():
+            raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+        self.device, self.stream = device, stream
+        self.raw = (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+    def empty(self, shape, dtype):
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def workspace(self, nbytes, workspace):
+        if workspace is None:
+            return self.empty(nbytes, torch.uint8)
+        if workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
+        return workspace
+
+
+def _nbytes(t) -> int:
+    return t.numel() * t.element_size()
+
+
+def paged_attn(q: torch.Tensor, G: int, cache: PagedKv, parent=None, n_nodes=None, window: int = 0, sinks: int = 0,
+               out=None, workspace=None, stream=None):
+    """Attention of a step's query tokens q [B, M, Hkv * G, D] (bf16, M <= 64) over the paged cache, whose
+    last entries they are: a tree of drafted tokens (``parent`` int32 [B, M]), a chain (``parent`` None)
+    or one token (M = 1); ``n_nodes`` int32 [B] where a sequence has fewer than M.  ``window`` > 0 limits
+    each query to the window's positions and the first ``sinks`` ones.
+    Returns (out [B, M, Hq, D] bf16, lse [B, M, Hq] f32, ws)."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, M, Hq, D]")
+    M, Hq = q.shape[1], cache.Hkv * G
+    dev = cache.device
+    _want(q, "q", torch.bfloat16, (cache.B, M, Hq, cache.D), dev)
+    if parent is not None:
+        _want(parent, "parent", torch.int32, (cache.B, M), dev)
+    if n_nodes is not None:
+        _want(n_nodes, "n_nodes", torch.int32, (cache.B,), dev)
+    on = _On(dev, stream)
+    if out is None:
+        o, lse = on.empty(q.shape, torch.bfloat16), on.empty((cache.B, M, Hq), torch.float32)
+    else:
+        o, lse = out
+        _want(o, "out", torch.bfloat16, q.shape, dev)
+        _want(lse, "lse", torch.float32, (cache.B, M, Hq), dev)
+    ws = on.workspace(0 if workspace is not None else paged_workspace_size(cache, G, M), workspace)
+    _check(lib.sgd_paged_attn(q.data_ptr(), G, M, cache._ref, None if parent is None else parent.data_ptr(),
+                              None if n_nodes is None else n_nodes.data_ptr(), window, sinks, o.data_ptr(),
+                              lse.data_ptr(), ws.data_ptr(), _nbytes(ws), on.raw), "sgd_paged_attn")
+    return o, lse, ws
+
+
+def verify_tree(p: torch.Tensor, tokens: torch.Tensor, parent: torch.Tensor, u_accept: torch.Tensor,
+                u_sample: torch.Tensor, q=None, n_nodes=None, out=None, workspace=None, stream=None):
+    """Drafted tokens against the target's distributions p [B, M, V] (f32 or bf16; ``q`` the draft's, None
+    for chosen drafts), tokens and parent int32 [B, M], random numbers u_accept [B, M] and u_sample [B].
+    Returns (n_path [B], path [B, M], next_token [B], ws), int32."""
+    if p.dim() != 3 or p.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("p must be a float32 or bfloat16 [B, M, V] tensor")
+    (B, M, V), dev, i32 = p.shape, p.device, torch.int32
+    _want(p, "p", p.dtype, p.shape, dev)
+    _want(tokens, "tokens", i32, (B, M), dev)
+    _want(parent, "parent", i32, (B, M), dev)
+    _want(u_accept, "u_accept", torch.float32, (B, M), dev)
+    _want(u_sample, "u_sample", torch.float32, (B,), dev)
+    if q is not None:
+        _want(q, "q", p.dtype, p.shape, dev)
+    if n_nodes is not None:
+        _want(n_nodes, "n_nodes", i32, (B,), dev)
+    on = _On(dev, stream)
+    if out is None:
+        n_path, path, token = on.empty((B,), i32), on.empty((B, M), i32), on.empty((B,), i32)
+    else:
+        n_path, path, token = out
+        _want(n_path, "n_path", i32, (B,), dev)
+        _want(path, "path", i32, (B, M), dev)
+        _want(token, "next_token", i32, (B,), dev)
+    ws = on.workspace(256, workspace)
+    _check(lib.sgd_verify_tree(p.data_ptr(), _DT[p.dtype], None if q is None else q.data_ptr(), B, M, V,
+                               tokens.data_ptr(), parent.data_ptr(), None if n_nodes is None else n_nodes.data_ptr(),
+                               u_accept.data_ptr(), u_sample.data_ptr(), n_path.data_ptr(), path.data_ptr(),
+                               token.data_ptr(), ws.data_ptr(), _nbytes(ws), on.raw), "sgd_verify_tree")
+    return n_path, path, token, ws
+
+
+def _new_lens(on: _On, cache: PagedKv, out):
+    if out is None:
+        return on.empty((cache.B,), torch.int32)
+    _want(out, "new_lens", torch.int32, (cache.B,), cache.device)
+    return out
+
+
+def _paged_ws(on: _On, cache: PagedKv, workspace):
+    return on.workspace(0 if workspace is not None else paged_workspace_size(cache), workspace)
+
+
+def pages_reserve(cache: PagedKv, add: torch.Tensor, out=None, workspace=None, stream=None):
+    """Pages for ``add`` int32 [B] more tokens of each row.  Returns (new_lens [B], ws)."""
+    _want(add, "add", torch.int32, (cache.B,), cache.device)
+    on = _On(cache.device, stream)
+    new, ws = _new_lens(on, cache, out), _paged_ws(on, cache, workspace)
+    _check(lib.sgd_pages_reserve(cache._ref, add.data_ptr(), new.data_ptr(), ws.data_ptr(), _nbytes(ws), on.raw),
+           "sgd_pages_reserve")
+    return new, ws
+
+
+def pages_append(cache: PagedKv, k_new: torch.Tensor, v_new: torch.Tensor, cu_new: torch.Tensor, workspace=None,
+                 stream=None):
+    """Writes k_new, v_new [Hkv, T_new, D] (bf16; row b's tokens cu_new[b] .. cu_new[b+1] - 1) as the last
+    entries of each row; an int8 cache takes their codes under its scales.  Returns ws."""
+    if k_new.dim() != 3:
+        raise ValueError("k_new must be [Hkv, T_new, D]")
+    shape = (cache.Hkv, k_new.shape[1], cache.D)
+    _want(k_new, "k_new", torch.bfloat16, shape, cache.device)
+    _want(v_new, "v_new", torch.bfloat16, shape, cache.device)
+    _want(cu_new, "cu_new", torch.int32, (cache.B + 1,), cache.device)
+    on = _On(cache.device, stream)
+    ws = on.workspace(256, workspace)
+    _check(lib.sgd_pages_append(cache._ref, k_new.data_ptr(), v_new.data_ptr(), cu_new.data_ptr(), k_new.shape[1],
+                                ws.data_ptr(), _nbytes(ws), on.raw), "sgd_pages_append")
+    return ws
+
+
+def pages_fork(cache: PagedKv, src: torch.Tensor, dst: torch.Tensor, workspace=None, stream=None):
+    """Row dst[i] becomes a copy of row src[i] (int32 [n]).  Returns ws."""
+    if src.dim() != 1:
+        raise ValueError("src must be [n]")
+    _want(src, "src", torch.int32, src.shape, cache.device)
+    _want(dst, "dst", torch.int32, src.shape, cache.device)
+    on = _On(cache.device, stream)
+    ws = _paged_ws(on, cache, workspace)
+    _check(lib.sgd_pages_fork(cache._ref, src.data_ptr(), dst.data_ptr(), src.shape[0], ws.data_ptr(), _nbytes(ws),
+                              on.raw), "sgd_pages_fork")
+    return ws
+
+
+def pages_release(cache: PagedKv, keep: torch.Tensor, workspace=None, stream=None):
+    """Every row gives back the pages behind its first ``keep`` int32 [B] tokens.  Returns ws."""
+    _want(keep, "keep", torch.int32, (cache.B,), cache.device)
+    on = _On(cache.device, stream)
+    ws = on.workspace(256, workspace)
+    _check(lib.sgd_pages_release(cache._ref, keep.data_ptr(), ws.data_ptr(), _nbytes(ws), on.raw), "sgd_pages_release")
+    return ws
+
+
+def pages_accept(cache: PagedKv, path: torch.Tensor, n_path: torch.Tensor, n_nodes: torch.Tensor, out=None,
+                 workspace=None, stream=None):
+    """Of each row's last n_nodes entries those of ``path`` [B, M] (its first n_path) stay, as verify_tree
+    returns them.  Returns (new_lens [B], ws)."""
+    if path.dim() != 2:
+        raise ValueError("path must be [B, M]")
+    M = path.shape[1]
+    _want(path, "path", torch.int32, (cache.B, M), cache.device)
+    _want(n_path, "n_path", torch.int32, (cache.B,), cache.device)
+    _want(n_nodes, "n_nodes", torch.int32, (cache.B,), cache.device)
+    on = _On(cache.device, stream)
+    new, ws = _new_lens(on, cache, out), on.workspace(256, workspace)
+    _check(lib.sgd_pages_accept(cache._ref, path.data_ptr(), n_path.data_ptr(), n_nodes.data_ptr(), M, new.data_ptr(),
+                                ws.data_ptr(), _nbytes(ws), on.raw), "sgd_pages_accept")
+    return new, ws
+
+
+def pages_keep(cache: PagedKv, idx: torch.Tensor, cu_kept: torch.Tensor, out=None, workspace=None, stream=None):
+    """Each row and KV head keeps the tokens ``idx`` [Hkv, kept_total], cu_kept [B + 1] (as oam_select
+    returns them) as its first ones.  Returns (new_lens [B], ws)."""
+    if idx.dim() != 2:
+        raise ValueError("idx must be [Hkv, kept_total]")
+    _want(idx, "idx", torch.int32, (cache.Hkv, idx.shape[1]), cache.device)
+    _want(cu_kept, "cu_kept", torch.int32, (cache.B + 1,), cache.device)
+    on = _On(cache.device, stream)
+    new, ws = _new_lens(on, cache, out), on.workspace(256, workspace)
+    _check(lib.sgd_pages_keep(cache._ref, idx.data_ptr(), cu_kept.data_ptr(), idx.shape[1], new.data_ptr(),
+                              ws.data_ptr(), _nbytes(ws), on.raw), "sgd_pages_keep")
+    return new, ws

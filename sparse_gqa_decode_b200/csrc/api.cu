@@ -172,6 +172,18 @@ void apply_test_hooks(DecodeArgs &a) {
     a.idle_producer = g_hooks.idle_producer;
 }
 
+void paged_test_hooks(long long *wait_limit, int *idle_producer) {
+    *wait_limit = g_hooks.wait_limit > 0 ? g_hooks.wait_limit : kWaitLimit;
+    *idle_producer = g_hooks.idle_producer;
+}
+
+int device_sms(int *sms) {
+    DevInfo *dev;
+    const int rc = current_device(&dev);
+    if (rc == SGD_OK) *sms = dev->sms;
+    return rc;
+}
+
 int kt_begin(cudaStream_t s) {
     if (!g_kt.on || g_kt.n >= (int)g_kt.fn.size()) return -1;
     const int k = g_kt.n;

@@ -110,4 +110,9 @@ int launch_stream_read(const void *buf, size_t bytes, int method, unsigned long 
 int launch_gather_read(const void *a, const void *b, int64_t row_bytes, const int32_t *rows, int64_t n_rows,
                        unsigned long long *sink, int sm_count, cudaStream_t s);
 
+// host state shared with the paged entry points (api.cu): the current device's SM count (an SGD_ERR_*
+// code where it is not sm_100) and the pipeline test hooks
+int device_sms(int *sms);
+void paged_test_hooks(long long *wait_limit, int *idle_producer);
+
 }  // namespace sgd
