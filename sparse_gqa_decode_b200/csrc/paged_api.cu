@@ -95,7 +95,8 @@ int sgd_paged_attn(const void *q, int G, int M, const sgd_paged_kv *kv, const in
     rc = begin(workspace, workspace_bytes, workspace_bytes_of(kv, G, M), true, s, &a.sms);
     if (rc != SGD_OK) return rc;
     a.q = q, a.parent = parent, a.n_nodes = n_nodes, a.out = out, a.lse = lse;
-    a.G = G, a.M = M, a.window = window, a.sinks = window ? sinks : 0;
+    // no position reaches 2^30 (max_pages < 2^24): larger values mean the same
+    a.G = G, a.M = M, a.window = std::min(window, 1 << 30), a.sinks = window ? std::min(sinks, 1 << 30) : 0;
     a.scale_log2 = (float)(1.4426950408889634 / sqrt((double)kv->D));
     a.ws = reinterpret_cast<uint8_t *>(scratch_of(workspace));
     a.status = status_of(workspace);
