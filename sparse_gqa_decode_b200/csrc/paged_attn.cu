@@ -12,8 +12,8 @@
 // each with its own S and O, merged at the end of the segment; so one computes its softmax while the
 // tensor cores work for the other.  More rows: two row tiles a CTA over the same KV tiles, and ranges
 // of ceil(rows / 256) CTAs side by side that read the same tiles at the same time (from L2 but the
-// first).  Either way the warpgroups g = 0, 1 alternate on the tensor cores:
-//   QK_0 QK_1 | PV_0 QK_0 PV_1 QK_1 | PV_0 QK_0 ...
+// first).  Either way the groups g = 0, 1 take turns on the tensor cores:
+//   QK_0 QK_1 | PV_0 QK_0 PV_1 QK_1 | PV_0 QK_0 ...   with the softmax of g between its QK and its PV.
 //
 // The work is cut without the host: every CTA sums the rows' tile counts itself (a window leaves the
 // tiles of the first tokens and of the window only), takes an equal range of the stream of all (row,
@@ -24,6 +24,11 @@
 // log2 (p then stays below 2^8, exact in range), which happens a few times in a long row, and
 // O is rescaled in tensor memory only then.  S, m, l and O are float32; P is rounded to bf16 (2^-8
 // relative), as is the output; l sums the unrounded p.
+//
+// INT8 codes are widened to f16 (exactly) in shared memory by warps of their own, a third fewer
+// instructions than to bf16.  So Q and P are f16 there: a row of Q is scaled by a power of two to a
+// maximum in [2^13, 2^14), which loses nothing but bits below 2^-38 of that maximum; P carries 2^7, so that
+// f16's smallest step, 2^-24, is 2^-31 of the largest p and what 2^17 tokens could lose stays below 2^-14.
 #include <math.h>
 #include <string.h>
 
@@ -43,7 +48,7 @@ namespace {
 constexpr int kTile = 128;       // tokens of a KV tile, rows of a row tile
 constexpr int kItemCharge = 2;   // tiles of work charged to an item beside its own (start, epilogue)
 constexpr float kSlack = 8.f;    // log2 by which the true maximum may pass the reference
-constexpr int kWarpProducer = 0, kWarpMma = 1, kWarpSoftmax = 4;  // softmax: warps 4..11
+constexpr int kWarpProducer = 0, kWarpMma = 1, kWarpSoftmax = 4, kWarpConvert = 12;  // softmax: 4..11
 
 // What a launch needs beside the cache and the arguments.
 struct AttnPlan {
@@ -86,6 +91,12 @@ __device__ __forceinline__ Seq seq_of(const PagedView &kv, const PagedAttnArgs &
     return s;
 }
 
+// Whether the tile at t0 has entries that no query of the sequence sees (behind its end, or between the first tokens
+// and the windows): they may hold anything, so that their V rows have to become 0 before the product.
+__device__ __forceinline__ bool has_unseen(const Seq &s, const PagedAttnArgs &a, int t0) {
+    return t0 + kTile > s.L || (a.window && t0 < s.base + 1 - a.window && t0 + kTile > a.sinks);
+}
+
 __device__ __forceinline__ int tile_of(const Seq &s, int v) { return v < s.sink_tiles ? v : v - s.sink_tiles + s.first; }
 
 // bits i of 0..31 with from <= i < to
@@ -107,14 +118,17 @@ struct Cfg {
     static constexpr int SLOTS = I8 ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 8);  // bf16 tiles of K or V
     static constexpr int RAW = I8 ? (D == 128 ? 4 : 8) : 0;                     // code tiles in flight
     static constexpr int RAW_BYTES = kTile * D;
-    static constexpr int THREADS = I8 ? 512 : 384;
+    static constexpr int CONVERT = I8 ? 128 : 0;         // threads that widen codes
+    static constexpr int THREADS = 384 + CONVERT;
     static constexpr int ROWS = TWO ? 256 : 128;
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_SLOT = Q_BUFS * TILE_BYTES;
     static constexpr int OFF_RAW = OFF_SLOT + SLOTS * TILE_BYTES;
     static constexpr int OFF_ML = OFF_RAW + RAW * RAW_BYTES;  // [2][128] (m, l) of the warpgroups
-    static constexpr int OFF_BAR = OFF_ML + 2 * 128 * 8;
+    static constexpr int OFF_QE = OFF_ML + 2 * 128 * 8;       // I8, one row tile: [128] the rows' powers of two
+    static constexpr int OFF_BAR = OFF_QE + 128 * 4;
     static constexpr int SMEM = OFF_BAR + 512;
+    static constexpr float SHIFT = I8 ? 7.f : 0.f;            // log2 that P carries
     static_assert(SMEM <= 232448, "fits a CTA's shared memory");
 };
 
@@ -122,12 +136,11 @@ struct Bars {
     uint64_t full[8], empty[8];          // ring of bf16 K / V tiles, in the order the products take them
     uint64_t raw_full[8], raw_empty[8];  // I8: ring of code tiles
     uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[2], p_full[2], o_full[2];
-    uint64_t o_free, ml_full, drained;
+    uint64_t s_full[2], v_here[2], p_full[2], o_full[2];
+    uint64_t q_ready, o_free, ml_full, drained;
     uint32_t tmem;
     int32_t abort;
     int32_t start_b, start_pos;          // the range's first row and its stream position
-    int32_t sm[33];
 };
 static_assert(sizeof(Bars) <= 512, "barriers fit their space");
 
@@ -140,6 +153,32 @@ __device__ __forceinline__ int pos_k(int j) {
 template <bool TWO>
 __device__ __forceinline__ int pos_v(int j, int T) {
     return TWO ? 2 * j + 1 : min(2 * j + 2, 2 * T - 1);
+}
+
+// Row r of a row tile of Q from bf16 to f16 in place, scaled by a power of two to a maximum in [2^13, 2^14); returns
+// its inverse.  A thread has its row to itself; eight threads' 16-byte pieces lie in different banks.
+template <class C>
+__device__ __forceinline__ float q_to_f16(uint8_t *q, int r) {
+    constexpr int N = C::D / 8;
+    auto piece = [&](int c) { return reinterpret_cast<uint4 *>(q + c / 8 * kTile * 128 + r * 128 + ((c % 8) ^ (r & 7)) * 16); };
+    uint32_t m = 0;
+#pragma unroll 4
+    for (int c = 0; c < N; ++c) {
+        const uint4 x = *piece(c);
+        m = bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(bf16x2_absmax(m, x.x), x.y), x.z), x.w);
+    }
+    const float top = bf16x2_fold_max(m);
+    // exponent of the maximum, 2^e <= top < 2^(e + 1); a zero, subnormal or infinite maximum takes the nearest normal
+    const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 126);
+    const float f = __uint_as_float((uint32_t)(127 + 13 - e) << 23);  // 2^(13 - e): 13 - e in [-113, 113]
+#pragma unroll 4
+    for (int c = 0; c < N; ++c) {
+        uint4 x = *piece(c);
+        auto half2 = [&](uint32_t w) { return pack_f16(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f); };
+        x.x = half2(x.x), x.y = half2(x.y), x.z = half2(x.z), x.w = half2(x.w);
+        *piece(c) = x;
+    }
+    return __uint_as_float((uint32_t)(127 - 13 + e) << 23);
 }
 
 // Walks a CTA's range: the same sequence of segments in every role.
@@ -203,20 +242,22 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
     if (tid == 0) {
         for (int i = 0; i < C::SLOTS; ++i) {
-            mbar_init(&bar.full[i], C::I8 ? 4 : 1);
+            mbar_init(&bar.full[i], C::I8 ? C::CONVERT / 32 : 1);
             mbar_init(&bar.empty[i], 1);
         }
         for (int i = 0; i < C::RAW; ++i) {
             mbar_init(&bar.raw_full[i], 1);
-            mbar_init(&bar.raw_empty[i], 4);
+            mbar_init(&bar.raw_empty[i], C::CONVERT / 32);
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(&bar.q_full[g], 1);
             mbar_init(&bar.q_empty[g], 1);
             mbar_init(&bar.s_full[g], 1);
+            mbar_init(&bar.v_here[g], 1);
             mbar_init(&bar.p_full[g], warps[g]);
             mbar_init(&bar.o_full[g], 1);
         }
+        mbar_init(&bar.q_ready, warps[0] + (C::TWO ? warps[1] : 0));
         mbar_init(&bar.o_free, warps[0] + warps[1]);
         mbar_init(&bar.ml_full, warps[0] + warps[1]);
         mbar_init(&bar.drained, 1);
@@ -239,7 +280,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         for (int b = b0; b < b1; ++b) sum += (seq_of(kv, a, b, bad).tiles + kItemCharge) * kv.Hkv;
         if (bad && blockIdx.x == 0) atomicOr(a.status, bad);
         int total;
-        int pos = block_exclusive_scan(sum, total, bar.sm);
+        int pos = block_exclusive_scan(sum, total, reinterpret_cast<int32_t *>(smem + C::OFF_ML));
         const int S = (total + plan.n_ranges - 1) / plan.n_ranges;
         x0 = min((int64_t)range * S, (int64_t)total);
         x1 = min(x0 + S, total);
@@ -260,7 +301,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
     volatile int32_t *abort = &bar.abort;
-    auto wait = [&](uint64_t *m, uint32_t parity) { return mbar_wait(m, parity, a.status, abort, a.wait_limit); };
+    // the first poll looks at nothing but the barrier: while the tensor cores read their operands a shared-memory
+    // access takes a few hundred cycles, and the abort flag would double that
+    auto wait = [&](uint64_t *m, uint32_t parity) {
+        return mbar_try_wait(m, parity) || mbar_wait(m, parity, a.status, abort, a.wait_limit);
+    };
     // the same answer in every lane, so that the warp stays together
     auto wait_warp = [&](uint64_t *m, uint32_t parity) { return (bool)__all_sync(0xffffffffu, wait(m, parity)); };
     Walk w;
@@ -336,93 +381,90 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
     } else if (warp == kWarpMma) {
         // ------------------------------------------------------------------ products
+        // One thread issues all products.  It waits for every KV tile, in ring order: a parity tells a barrier's
+        // phases apart only for a thread that misses none.  A wait costs a few hundred cycles here even where its
+        // barrier is done (the tensor cores' operand reads fill the shared memory's time), so a tile's V, and with two
+        // row tiles the next K, is waited for before its P, while the softmax is at work: 318 -> 264 us for 512 rows
+        // and 4 x 31K tokens.  An issuing warp for each group instead took 320 us.
         if (lane == 0) {
-            constexpr uint32_t ID_QK = tc_idesc_bf16(128, kTile, false), ID_PV = tc_idesc_bf16(128, D, true);
+            constexpr uint32_t ID_QK = tc_idesc(C::I8, 128, kTile, false), ID_PV = tc_idesc(C::I8, 128, D, true);
             const uint32_t sq = smem_u32(smem + C::OFF_Q), ss = smem_u32(smem + C::OFF_SLOT);
             uint32_t at = 0, seg = 0, np[2] = {0, 0};
             bool go = true;
-            auto full = [&](uint32_t pos) {
-                if (go) go = wait(&bar.full[pos % C::SLOTS], (pos / C::SLOTS) & 1);
-                return go;
-            };
+            auto slot = [&](uint32_t pos) { return ss + (pos % C::SLOTS) * C::TILE_BYTES; };
+            auto full = [&](uint32_t pos) { return go && (go = wait(&bar.full[pos % C::SLOTS], (pos / C::SLOTS) & 1)); };
+            auto release = [&](uint32_t pos) { tc_commit(&bar.empty[pos % C::SLOTS]); };
             auto qk = [&](int g, uint32_t q, uint32_t pos) {  // S_g = Q K^T
-                const uint32_t k = ss + (pos % C::SLOTS) * C::TILE_BYTES;
                 tc_fence_after();
+                const uint64_t dq = desc_k_major(q), dk = desc_k_major(slot(pos));
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
-                    const uint32_t off = (j / 4) * (kTile * 128) + (j % 4) * 32;
-                    mma_ss(tmem + g * 128, desc_k_major(q + off), desc_k_major(k + off), ID_QK, j > 0);
+                    const uint32_t off = ((j / 4) * (kTile * 128) + (j % 4) * 32) >> 4;  // in the descriptors' 16 bytes
+                    mma_ss(tmem + g * 128, dq + off, dk + off, ID_QK, j > 0);
                 }
+                tc_commit(&bar.s_full[g]);
             };
             auto pv = [&](int g, uint32_t pos, bool acc) {  // O_g (+)= P_g V
-                const uint32_t v = ss + (pos % C::SLOTS) * C::TILE_BYTES;
+                if (!go || !(go = wait(&bar.p_full[g], np[g]++ & 1))) return false;
                 tc_fence_after();
+                const uint64_t dv = desc_mn_major(slot(pos), kTile * 128);
 #pragma unroll
                 for (int j = 0; j < kTile / 16; ++j)
-                    mma_ts(tmem + 256 + g * 128, tmem + g * 128 + j * 8, desc_mn_major(v + j * 2048, kTile * 128), ID_PV,
-                           acc || j > 0);
-            };
-            auto release = [&](uint32_t pos) { tc_commit(&bar.empty[pos % C::SLOTS]); };
-            auto p_ready = [&](int g) {
-                if (go) go = wait(&bar.p_full[g], np[g]++ & 1);
-                return go;
+                    mma_ts(tmem + 256 + g * 128, tmem + g * 128 + j * 8, dv + j * (2048 >> 4), ID_PV, acc || j > 0);
+                return true;
             };
             while (go && w.next(kv, a)) {
                 const int T = w.hi - w.lo, qs = seg % C::Q_STAGES;
-                if (!wait(&bar.q_full[qs], (seg / C::Q_STAGES) & 1)) break;
+                go = C::I8 ? wait(&bar.q_ready, seg & 1) : wait(&bar.q_full[qs], (seg / C::Q_STAGES) & 1);
+                if (!go) break;
                 const uint32_t q0 = sq + (C::TWO ? 0 : qs) * C::TILE_BYTES;
-                auto o_free = [&](int j, int first) {  // before a segment's first PV: the last one's O was read
-                    if (j == first && seg > 0 && go) go = wait(&bar.o_free, (seg - 1) & 1);
-                    return go;
-                };
                 if constexpr (C::TWO) {
                     if (!full(at)) break;
-                    for (int g = 0; g < 2; ++g) {
-                        qk(g, q0 + g * C::TILE_BYTES, at);
-                        tc_commit(&bar.s_full[g]);
-                    }
+                    for (int g = 0; g < 2; ++g) qk(g, q0 + g * C::TILE_BYTES, at);
                     release(at);
-                    if (T == 1) tc_commit(&bar.q_empty[qs]);
-                    for (int j = 0; j < T; ++j) {
-                        const uint32_t pv_at = at + pos_v<true>(j, T), k_at = at + pos_k<true>(j + 1);
-                        for (int g = 0; g < 2; ++g) {
-                            if (!o_free(j, 0) || !p_ready(g) || !full(pv_at)) break;
-                            pv(g, pv_at, j > 0);
-                            if (j + 1 < T) {
-                                if (!full(k_at)) break;
-                                qk(g, q0 + g * C::TILE_BYTES, k_at);
-                                tc_commit(&bar.s_full[g]);
-                            } else {
-                                tc_commit(&bar.o_full[g]);
-                            }
-                        }
-                        if (!go) break;
-                        release(pv_at);
-                        if (j + 1 < T) release(k_at);
-                        if (j + 2 == T) tc_commit(&bar.q_empty[qs]);
-                    }
+                    if (T == 1) tc_commit(&bar.q_empty[qs]);  // the last product that reads Q was issued
                 } else {
                     for (int g = 0; g < min(T, 2); ++g) {
                         if (!full(at + g)) break;
                         qk(g, q0, at + g);
                         release(at + g);
-                        tc_commit(&bar.s_full[g]);
                     }
+                    if (!go) break;
                     if (T <= 2) tc_commit(&bar.q_empty[qs]);
-                    for (int j = 0; go && j < T; ++j) {
+                }
+                if (seg > 0 && !(go = wait(&bar.o_free, (seg - 1) & 1))) break;  // the last segment's O was read
+                for (int j = 0; j < T; ++j) {
+                    const uint32_t v_at = at + pos_v<C::TWO>(j, T), k_at = at + pos_k<C::TWO>(C::TWO ? j + 1 : j + 2);
+                    const bool unseen = has_unseen(w.s, a, tile_of(w.s, w.lo + j) * kTile);
+                    if (!full(v_at)) break;
+                    if constexpr (C::TWO) {
+                        const bool more = j + 1 < T;
+                        if (unseen) {  // the softmax warps may clear its rows
+                            mbar_arrive(&bar.v_here[0]);
+                            mbar_arrive(&bar.v_here[1]);
+                        }
+                        if (more && !full(k_at)) break;
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            if (!pv(g, v_at, j > 0)) break;
+                            if (more) qk(g, q0 + g * C::TILE_BYTES, k_at);
+                            else tc_commit(&bar.o_full[g]);
+                        }
+                        if (!go) break;
+                        release(v_at);
+                        if (more) release(k_at);
+                        if (j + 2 == T) tc_commit(&bar.q_empty[qs]);
+                    } else {
                         const int g = j & 1;
-                        const uint32_t pv_at = at + pos_v<false>(j, T), k_at = at + pos_k<false>(j + 2);
-                        if (!o_free(j, 0) || !p_ready(g) || !full(pv_at)) break;
-                        pv(g, pv_at, j > 1);
-                        release(pv_at);
+                        if (unseen) mbar_arrive(&bar.v_here[g]);
+                        if (!pv(g, v_at, j > 1)) break;
+                        if (j + 2 >= T) tc_commit(&bar.o_full[g]);
+                        release(v_at);
                         if (j + 2 < T) {
                             if (!full(k_at)) break;
                             qk(g, q0, k_at);
                             release(k_at);
-                            tc_commit(&bar.s_full[g]);
                             if (j + 3 == T) tc_commit(&bar.q_empty[qs]);
-                        } else {
-                            tc_commit(&bar.o_full[g]);
                         }
                     }
                 }
@@ -443,13 +485,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const int m = (C::TWO ? rt * 2 + g : 0) * plan.Mt + r / a.G, gh = r % a.G;
             const uint32_t lane_at = tmem + ((uint32_t)(wq * 32) << 16);
             const uint32_t ts = lane_at + g * 128, to = lane_at + 256 + g * 128;
-            float scale = a.scale_log2, vs = 1.f;
+            float scale = a.scale_log2, vs = 1.f, scale_k = scale;
             if constexpr (C::I8) {
                 const bool report = blockIdx.x == 0 && g == 0 && r == 0;
-                scale *= calibrated_scale(kv.k_scale, a.status, report);
+                scale_k *= calibrated_scale(kv.k_scale, a.status, report);
                 vs = calibrated_scale(kv.v_scale, a.status, report);
             }
-            uint32_t at = 0, seg = 0, ns = 0, no[2] = {0, 0};
+            uint32_t at = 0, seg = 0, ns = 0, nv = 0, no[2] = {0, 0};
             float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
             int lo = 0;          // the first entry of the row's window
             uint64_t sees = 0;   // the nodes that the row sees
@@ -489,6 +531,24 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         if (bad) atomicOr(a.status, bad);
                     }
                 }
+                if constexpr (C::I8) {  // the row of Q as f16, scaled by 2^-e
+                    const int qs = seg % C::Q_STAGES;
+                    float *qe = reinterpret_cast<float *>(smem + C::OFF_QE);
+                    if (C::TWO || g == 0) {
+                        if (!(go = wait_warp(&bar.q_full[qs], (seg / C::Q_STAGES) & 1))) break;
+                        if (valid) {
+                            const float f = q_to_f16<C>(smem + C::OFF_Q + (C::TWO ? g : qs) * C::TILE_BYTES, r);
+                            scale = scale_k * f;
+                            if constexpr (!C::TWO) qe[r] = f;
+                        }
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.q_ready);
+                    } else {
+                        if (!(go = wait_warp(&bar.q_ready, seg & 1))) break;
+                        if (valid) scale = scale_k * qe[r];
+                    }
+                }
                 const bool query = valid && m < s.n;
                 const int prefix = query && s.base > 0 ? s.base : 0;  // entries before the nodes that the row may see
                 const int sink = min(a.sinks, prefix);
@@ -496,25 +556,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 float mx = -INFINITY, l = 0.f;
                 for (int j = C::TWO ? 0 : g; j < T; j += C::TWO ? 1 : 2) {
                     const int t0 = tile_of(s, w.lo + j) * kTile;
-                    // entries that no row sees may hold anything: their V rows become 0
-                    const bool clean = t0 + kTile > s.L || (a.window && t0 < v_lo && t0 + kTile > a.sinks);
-                    if (clean) {
-                        const uint32_t pos = at + pos_v<C::TWO>(j, T);
-                        if (!(go = wait_warp(&bar.full[pos % C::SLOTS], (pos / C::SLOTS) & 1))) break;
-                        uint8_t *v = smem + C::OFF_SLOT + (pos % C::SLOTS) * C::TILE_BYTES;
-                        for (int i = wq; i < kTile; i += na) {
-                            const int t = t0 + i;
-                            if ((t >= s.L || (a.window && t >= a.sinks && t < v_lo)) && lane < D / 8)
-                                *reinterpret_cast<uint4 *>(v + (lane / 8) * kTile * 128 + i * 128 + (lane % 8) * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async_shared();
-                    }
                     if (!(go = wait_warp(&bar.s_full[g], ns & 1))) break;
                     ++ns;
                     tc_fence_after();
+                    // rows that ask nothing do not count: whatever they gather is dropped at the end
                     const bool masked = __any_sync(
-                        0xffffffffu, t0 + kTile > prefix || (lo > t0 && t0 + kTile > sink));
+                        0xffffffffu, query && (t0 + kTile > prefix || (lo > t0 && t0 + kTile > sink)));
                     auto mask_of = [&](int c) {  // the row's entries among the 32 from t0 + 32 c
                         const int tw = t0 + c * 32, off = s.base - tw;
                         uint32_t k = bits(lo - tw, prefix - tw) | bits(-tw, sink - tw);
@@ -527,55 +574,59 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     };
                     // the row's maximum
                     float top = -INFINITY;
-                    if (masked) {
+                    if (!masked) {
+#pragma unroll 1
+                        for (int c = 0; c < 4; c += 2) {
+                            uint32_t x[32], y[32];
+                            tmem_ld32(x, ts + c * 32);
+                            tmem_ld32(y, ts + c * 32 + 32);
+                            tmem_wait_ld(x);
+                            tmem_wait_ld(y);
+                            float t4[4] = {top, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                t4[i & 3] = max3(t4[i & 3], __uint_as_float(x[i]), __uint_as_float(y[i]));
+                            top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                        }
+                    } else {
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
                             uint32_t x[32];
                             tmem_ld32(x, ts + c * 32);
-                            tmem_wait_ld();
+                            tmem_wait_ld(x);
                             const uint32_t k = mask_of(c);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) top = fmaxf(top, k >> i & 1 ? __uint_as_float(x[i]) : -INFINITY);
                         }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t x[32];
-                            tmem_ld32(x, ts + c * 32);
-                            tmem_wait_ld();
-                            float t4[4] = {top, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) t4[i & 3] = fmaxf(t4[i & 3], __uint_as_float(x[i]));
-                            top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-                        }
                     }
                     const float mt = top == -INFINITY ? -INFINITY : top * scale;
                     const bool first = j < 2 && (C::TWO ? j == 0 : true);
-                    if (__any_sync(0xffffffffu, mt > mx + kSlack)) {
+                    if (__any_sync(0xffffffffu, query && mt > mx + kSlack)) {
                         const float m2 = fmaxf(mx, mt), f = mx == -INFINITY ? 0.f : ex2(mx - m2);
                         mx = m2;
                         l *= f;
                         if (!first) {
 #pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t x[32];
-                                tmem_ld32(x, to + c * 32);
-                                tmem_wait_ld();
+                            for (int c = 0; c < D / 8; ++c) {  // 8 at a time: a row of S is held meanwhile
+                                uint32_t y[8];
+                                tmem_ld8(y, to + c * 8);
+                                tmem_wait_ld(y);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                                tmem_st32(to + c * 32, x);
+                                for (int i = 0; i < 8; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+                                tmem_st8(to + c * 8, y);
                             }
                         }
                     }
-                    const float ref = mx == -INFINITY ? 0.f : mx;
+                    const float ref = (mx == -INFINITY ? 0.f : mx) - C::SHIFT;
                     // p, its sum, and P in the place of S (a chunk's columns of P lie among those of S read before)
-                    float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                    auto pack = [](float p0, float p1) { return C::I8 ? pack_f16(p0, p1) : pack_bf16(p0, p1); };
                     if (masked) {
+                        float l4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
                         for (int c = 0; c < 4; ++c) {
                             uint32_t x[32], y[16];
                             tmem_ld32(x, ts + c * 32);
-                            tmem_wait_ld();
+                            tmem_wait_ld(x);
                             const uint32_t k = mask_of(c);
 #pragma unroll
                             for (int i = 0; i < 32; i += 2) {
@@ -583,28 +634,55 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                 const float p1 = k >> (i + 1) & 1 ? ex2(fmaf(__uint_as_float(x[i + 1]), scale, -ref)) : 0.f;
                                 l4[i & 2] += p0;
                                 l4[(i & 2) + 1] += p1;
-                                y[i / 2] = pack_bf16(p0, p1);
+                                y[i / 2] = pack(p0, p1);
                             }
                             tmem_st16(ts + c * 16, y);
                         }
+                        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
                     } else {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t x[32], y[16];
-                            tmem_ld32(x, ts + c * 32);
-                            tmem_wait_ld();
+                        float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                        auto chunk = [&](const uint32_t (&x)[32], int c) {
+                            uint32_t y[16];
 #pragma unroll
                             for (int i = 0; i < 32; i += 2) {
                                 const float p0 = ex2(fmaf(__uint_as_float(x[i]), scale, -ref));
                                 const float p1 = ex2(fmaf(__uint_as_float(x[i + 1]), scale, -ref));
                                 l4[i & 2] += p0;
                                 l4[(i & 2) + 1] += p1;
-                                y[i / 2] = pack_bf16(p0, p1);
+                                y[i / 2] = pack(p0, p1);
                             }
                             tmem_st16(ts + c * 16, y);
+                        };
+                        // the next chunk's load runs beside this one's exponentials
+                        uint32_t x0[32], x1[32];
+                        tmem_ld32(x0, ts);
+                        tmem_wait_ld(x0);
+#pragma unroll 1
+                        for (int c = 0; c < 4; c += 2) {
+                            tmem_ld32(x1, ts + c * 32 + 32);
+                            chunk(x0, c);
+                            tmem_wait_ld(x1);
+                            if (c == 0) tmem_ld32(x0, ts + 64);
+                            chunk(x1, c + 1);
+                            if (c == 0) tmem_wait_ld(x0);
                         }
+                        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
                     }
-                    l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                    if (has_unseen(s, a, t0)) {  // clear V's rows once they are here
+                        if (!(go = wait_warp(&bar.v_here[g], nv++ & 1))) break;
+                        const uint32_t pos = at + pos_v<C::TWO>(j, T);
+                        uint8_t *v = smem + C::OFF_SLOT + (pos % C::SLOTS) * C::TILE_BYTES;
+                        auto zero = [&](int from, int to) {  // rows of the tile, 16 bytes a lane
+                            constexpr int PER = D / 8;
+                            from = max(from, 0), to = min(to, kTile);
+                            for (int u = from * PER + wq * 32 + lane; u < to * PER; u += na * 32)
+                                *reinterpret_cast<uint4 *>(v + (u % PER) / 8 * kTile * 128 + u / PER * 128 + u % 8 * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                        };
+                        zero(s.L - t0, kTile);
+                        if (a.window) zero(a.sinks - t0, min(v_lo, s.L) - t0);
+                        fence_proxy_async_shared();
+                    }
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
@@ -612,13 +690,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
                 if (!go) break;
 
+                if (!query) l = 0.f;
+
                 // the segment's result
                 const bool whole = w.lo == 0 && w.hi == s.tiles;
                 const int64_t out_row = (((int64_t)w.b * a.M + m) * kv.Hkv + w.h) * a.G + gh;
                 const int64_t part_row =
                     ((int64_t)blockIdx.x * 2 + (w.lo == 0)) * C::ROWS + (C::TWO ? g * 128 : 0) + r;
                 float f0, f1 = 0.f, sum, ref;  // O_0 f0 + O_1 f1 is the normalised row
-                constexpr int NO = C::TWO ? 1 : 2;
                 if constexpr (C::TWO) {
                     sum = l, ref = mx;
                     f0 = sum > 0.f ? vs / sum : 0.f;
@@ -643,34 +722,32 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (!go) break;
                 tc_fence_after();
                 // TWO: the row's D channels; else this group's half of them, from both accumulators
-                constexpr int NC = C::TWO ? D / 32 : D / 64;
+                constexpr int NC = (C::TWO ? D : D / 2) / 16;
 #pragma unroll 1
                 for (int c = 0; c < NC; ++c) {
-                    const int col = C::TWO ? c * 32 : g * (D / 2) + c * 32;
-                    uint32_t x[32];
-                    float o[32];
-                    tmem_ld32(x, lane_at + 256 + (C::TWO ? g * 128 : 0) + col);
-                    tmem_wait_ld();
+                    const int col = (C::TWO ? 0 : g * (D / 2)) + c * 16;
+                    uint32_t x[16];
+                    float o[16];
+                    tmem_ld16(x, lane_at + 256 + (C::TWO ? g * 128 : 0) + col);
+                    tmem_wait_ld(x);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = f0 != 0.f ? f0 * __uint_as_float(x[i]) : 0.f;
-                    if constexpr (NO == 2) {
-                        if (T > 1) {
-                            tmem_ld32(x, lane_at + 256 + 128 + col);
-                            tmem_wait_ld();
+                    for (int i = 0; i < 16; ++i) o[i] = f0 != 0.f ? f0 * __uint_as_float(x[i]) : 0.f;
+                    if (!C::TWO && T > 1) {
+                        tmem_ld16(x, lane_at + 256 + 128 + col);
+                        tmem_wait_ld(x);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] += f1 != 0.f ? f1 * __uint_as_float(x[i]) : 0.f;
-                        }
+                        for (int i = 0; i < 16; ++i) o[i] += f1 != 0.f ? f1 * __uint_as_float(x[i]) : 0.f;
                     }
                     if (valid && whole) {
                         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + out_row * D + col);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                        for (int i = 0; i < 2; ++i)
                             dst[i] = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
                                                 pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
                     } else if (valid) {
                         float4 *dst = reinterpret_cast<float4 *>(plan.o_part + part_row * D + col);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        for (int i = 0; i < 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                     __syncwarp();
                 }
@@ -678,7 +755,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.o_free);
                 if (valid && (C::TWO || g == 0)) {
-                    const float lse2 = sum > 0.f ? ref + log2f(sum) : -INFINITY;
+                    const float lse2 = sum > 0.f ? ref - C::SHIFT + log2f(sum) : -INFINITY;
                     if (whole) a.lse[out_row] = lse2 * 0.69314718055994531f;
                     else plan.lse_part[part_row] = lse2;
                 }
@@ -690,12 +767,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 ++seg;
             }
         }
-    } else if (C::I8 && warp >= 12) {
-        // ------------------------------------------------------------------ codes to bf16
-        // u = 0x4300 | byte is the bf16 number 128 + (byte & 127) with the sign bit where 256's
-        // exponent differs from 128's: (u without bit 7) - (u without bits 0-6) = byte as a signed number,
-        // exactly
-        const int ct = tid - 12 * 32;
+    } else if (C::I8 && warp >= kWarpConvert) {
+        // ------------------------------------------------------------------ codes to f16
+        const int ct = tid - kWarpConvert * 32;
         uint32_t at = 0;
         bool go = true;
         while (go && w.next(kv, a)) {
@@ -707,30 +781,30 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (at >= C::SLOTS && !(go = wait_warp(&bar.empty[bs], (at / C::SLOTS - 1) & 1))) break;
                 const uint8_t *src = smem + C::OFF_RAW + rs * C::RAW_BYTES;
                 uint8_t *dst = smem + C::OFF_SLOT + bs * C::TILE_BYTES;
-                constexpr int UNITS = kTile * D / 16;  // 16 codes each
-#pragma unroll 2
-                for (int u = ct; u < UNITS; u += 128) {
-                    const int row = u / (D / 16), cb = u % (D / 16);
-                    const uint4 x = *reinterpret_cast<const uint4 *>(src + u * 16);
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t y[8];
+                constexpr int UNITS = kTile * D / 16, U = 4;  // 16 codes each; U loads of a thread in flight
+#pragma unroll 1
+                for (int u0 = ct; u0 < UNITS; u0 += 128 * U) {
+                    uint4 x[U];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const uint32_t e = __byte_perm(xs[k / 2], 0x43434343u, k & 1 ? 0x4342 : 0x4140);
-                        const uint32_t hi = e & 0xff7fff7fu, lo = e & 0xff80ff80u;
-                        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&hi),
-                                                         *reinterpret_cast<const __nv_bfloat162 *>(&lo));
-                        y[k] = *reinterpret_cast<const uint32_t *>(&d);
-                    }
-                    // two 16-byte pieces of the swizzled row; the second half's threads start with the odd one, so
-                    // that a quarter warp's stores cover all banks
-                    uint8_t *base = dst + (cb / 4) * (kTile * 128) + row * 128;
-                    const int ch = (cb % 4) * 2, odd = cb / 4 & 1;
+                    for (int i = 0; i < U; ++i) x[i] = *reinterpret_cast<const uint4 *>(src + (u0 + 128 * i) * 16);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int e = k ^ odd;
-                        *reinterpret_cast<uint4 *>(base + (((ch + e) ^ (row & 7)) * 16)) =
-                            e ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
+                    for (int i = 0; i < U; ++i) {
+                        const int u = u0 + 128 * i, row = u / (D / 16), cb = u % (D / 16);
+                        uint32_t y[8];
+                        s8x4_to_f16x2x2(x[i].x, y[0], y[1]);
+                        s8x4_to_f16x2x2(x[i].y, y[2], y[3]);
+                        s8x4_to_f16x2x2(x[i].z, y[4], y[5]);
+                        s8x4_to_f16x2x2(x[i].w, y[6], y[7]);
+                        // two 16-byte pieces of the swizzled row; the second half's threads start with the odd one, so
+                        // that a quarter warp's stores cover all banks
+                        uint8_t *base = dst + (cb / 4) * (kTile * 128) + row * 128;
+                        const int ch = (cb % 4) * 2, odd = cb / 4 & 1;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int e = k ^ odd;
+                            *reinterpret_cast<uint4 *>(base + (((ch + e) ^ (row & 7)) * 16)) =
+                                e ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
+                        }
                     }
                 }
                 fence_proxy_async_shared();
@@ -751,27 +825,31 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
 }
 
-// Joins the partial rows of an item that several ranges share: one CTA per output row, its warps take
-// the ranges in turn.  lse = log2 sum_c 2^lse_c, out = sum_c 2^(lse_c - lse) o_c.
-template <int D>
-__global__ void __launch_bounds__(128) paged_merge_kernel(PagedView kv, PagedAttnArgs a, AttnPlan plan, int two) {
-    __shared__ float so[4][D], sl[4], sm[4];
+// Joins the partial rows of an item that several ranges share: WARPS warps per output row take its
+// ranges in turn, four at a time.  lse = log2 sum_c 2^lse_c, out = sum_c 2^(lse_c - lse) o_c.
+constexpr int kMergeThreads = 256;
+
+template <int D, int WARPS>
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(PagedView kv, PagedAttnArgs a, AttnPlan plan,
+                                                                    int two, int64_t n_rows) {
+    constexpr int ROWS = kMergeThreads / 32 / WARPS;  // output rows of a CTA
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wr = warp % WARPS;
     const int Hq = kv.Hkv * a.G;
-    const int64_t out_row = blockIdx.x;
+    const int64_t out_row = (int64_t)blockIdx.x * ROWS + warp / WARPS;
+    if (out_row >= n_rows) return;  // WARPS > 1: ROWS is 1, the CTA leaves as a whole
     const int hq = (int)(out_row % Hq), m = (int)(out_row / Hq % a.M), b = (int)(out_row / Hq / a.M);
     const int2 it = plan.item[b * kv.Hkv + hq / a.G];
-    if (it.x == it.y || it.x < 0 || it.y >= plan.n_ranges || it.x > it.y) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (it.x >= it.y || it.x < 0 || it.y >= plan.n_ranges) return;  // written by its only range
     const int mt = m / plan.Mt, rt = two ? mt / 2 : 0, rows = two ? 256 : 128;
     const int r = (two ? mt % 2 * 128 : 0) + (m % plan.Mt) * a.G + hq % a.G;
     constexpr int E = D / 32;
     float mx = -INFINITY, l = 0.f, o[E] = {};
     constexpr int U = 4;
-    for (int c0 = it.x + warp; c0 <= it.y; c0 += 4 * U) {
+    for (int c0 = it.x + wr; c0 <= it.y; c0 += WARPS * U) {
         float z[U], x[U][E];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int c = c0 + 4 * u;
+            const int c = c0 + WARPS * u;
             z[u] = -INFINITY;
             if (c <= it.y) {
                 const int64_t row = (((int64_t)c * plan.RT + rt) * 2 + (c == it.x)) * rows + r;
@@ -795,24 +873,32 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(PagedView kv, PagedAtt
             for (int i = 0; i < E; ++i) o[i] = o[i] * f + e * x[u][i];
         }
     }
-    if (lane == 0) sm[warp] = mx, sl[warp] = l;
+    if constexpr (WARPS > 1) {
+        __shared__ float so[WARPS][D], sl[WARPS], sm[WARPS];
+        if (lane == 0) sm[warp] = mx, sl[warp] = l;
 #pragma unroll
-    for (int i = 0; i < E; ++i) so[warp][lane * E + i] = o[i];
-    __syncthreads();
-    const float top = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    float f[4], sum = 0.f;
+        for (int i = 0; i < E; ++i) so[warp][lane * E + i] = o[i];
+        __syncthreads();
+        if (warp != 0) return;
+        mx = -INFINITY;
+        for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, sm[w]);
+        l = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        f[i] = sl[i] > 0.f ? ex2(sm[i] - top) : 0.f;
-        sum += f[i] * sl[i];
+        for (int i = 0; i < E; ++i) o[i] = 0.f;
+        for (int w = 0; w < WARPS; ++w) {
+            const float f = sl[w] > 0.f ? ex2(sm[w] - mx) : 0.f;
+            l += f * sl[w];
+#pragma unroll
+            for (int i = 0; i < E; ++i) o[i] += f * so[w][lane * E + i];
+        }
     }
-    if (threadIdx.x < D) {
-        float x = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x += f[i] * so[i][threadIdx.x];
-        static_cast<__nv_bfloat16 *>(a.out)[out_row * D + threadIdx.x] = __float2bfloat16(sum > 0.f ? x / sum : 0.f);
-    }
-    if (threadIdx.x == 0) a.lse[out_row] = sum > 0.f ? (top + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+    const float f = l > 0.f ? 1.f / l : 0.f;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) + out_row * D) + lane * (E / 2);
+    if constexpr (E == 4)
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f));
+    else
+        *dst = pack_bf16(o[0] * f, o[1] * f);
+    if (lane == 0) a.lse[out_row] = l > 0.f ? (mx + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 // ------------------------------------------------------------------------------------------ host
@@ -877,7 +963,14 @@ int launch(const PagedView &kv, const PagedAttnArgs &a, const AttnPlan &plan, cu
     const cudaError_t e = launch_k(kern, dim3(plan.n_ranges * plan.RT), dim3(C::THREADS), C::SMEM, s, 1, kv, a, plan,
                                    mq, mk, mv);
     if (e != cudaSuccess) return SGD_ERR_CUDA;
-    launch_k(paged_merge_kernel<C::D>, dim3(kv.B * a.M * kv.Hkv * a.G), dim3(128), 0, s, 1, kv, a, plan, (int)C::TWO);
+    // few rows may have many ranges each (up to all of them): then a CTA per row; many rows have few
+    const int64_t n_rows = (int64_t)kv.B * a.M * kv.Hkv * a.G;
+    constexpr int W = kMergeThreads / 32;
+    if (n_rows <= 2048)
+        launch_k(paged_merge_kernel<C::D, W>, dim3((unsigned)n_rows), dim3(kMergeThreads), 0, s, 1, kv, a, plan, (int)C::TWO, n_rows);
+    else
+        launch_k(paged_merge_kernel<C::D, 1>, dim3((unsigned)((n_rows + W - 1) / W)), dim3(kMergeThreads), 0, s, 1, kv, a, plan,
+                 (int)C::TWO, n_rows);
     return cudaGetLastError() == cudaSuccess ? SGD_OK : SGD_ERR_CUDA;
 }
 

@@ -19,7 +19,13 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t addr, uint32_t columns) {
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for the calling warp's loads; `r` is what one of them brings, so that no use of it moves before the wait.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 32 columns of the calling lane's row (a warp reads the 32 lanes of its quarter, warp index mod 4)
@@ -35,16 +41,25 @@ __device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
         : "r"(addr));
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t (&r)[8], uint32_t addr) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
@@ -70,9 +85,9 @@ __device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr, uint32_t group)
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-// Instruction descriptor: bf16 x bf16 -> f32, M x N, B K-major or MN-major.
-constexpr uint32_t tc_idesc_bf16(int M, int N, bool b_mn_major) {
-    return 1u << 4 | 1u << 7 | 1u << 10 | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 |
+// Instruction descriptor: f16 x f16 or bf16 x bf16 -> f32, M x N, B K-major or MN-major.
+constexpr uint32_t tc_idesc(bool f16, int M, int N, bool b_mn_major) {
+    return 1u << 4 | (f16 ? 0u : 1u << 7 | 1u << 10) | (b_mn_major ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 |
            (uint32_t)(M >> 4) << 24;
 }
 
@@ -101,10 +116,63 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
                  : "memory");
 }
 
+// The calling warpgroup's registers per thread.  The shares of a block's warpgroups may not pass what
+// it was launched with.
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// two floats in a register pair, and packed arithmetic on them
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    return (uint64_t)__float_as_uint(lo) | (uint64_t)__float_as_uint(hi) << 32;
+}
+__device__ __forceinline__ float lo_of(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float hi_of(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// 2^x of two floats on the multiply-add units, for x <= 127 (below -126 as -126): x = n + r with n the
+// nearest integer, |r| <= 1/2, 2^r by the degree-5 polynomial of least relative error there (1.5e-7
+// with these float32 coefficients, found by Lawson's reweighted least squares), n into the exponent.
+__device__ __forceinline__ uint64_t ex2_poly2(uint64_t x) {
+    const float magic = 12582912.f;  // 1.5 * 2^23: adding it leaves n in the low mantissa bits
+    x = pair(fmaxf(lo_of(x), -126.f), fmaxf(hi_of(x), -126.f));
+    const uint64_t t = add2(x, pair(magic, magic));
+    const uint64_t r = fma2(add2(t, pair(-magic, -magic)), pair(-1.f, -1.f), x);
+    uint64_t p = pair(1.3276472454890609e-03f, 1.3276472454890609e-03f);
+    p = fma2(p, r, pair(9.675541892647743e-03f, 9.675541892647743e-03f));
+    p = fma2(p, r, pair(5.550713092088699e-02f, 5.550713092088699e-02f));
+    p = fma2(p, r, pair(2.4022120237350464e-01f, 2.4022120237350464e-01f));
+    p = fma2(p, r, pair(6.931469440460205e-01f, 6.931469440460205e-01f));
+    p = fma2(p, r, pair(1.0000001192092896f, 1.0000001192092896f));
+    const uint32_t lo = (uint32_t)p + ((uint32_t)t << 23);
+    const uint32_t hi = (uint32_t)(p >> 32) + ((uint32_t)(t >> 32) << 23);
+    return (uint64_t)lo | (uint64_t)hi << 32;
 }
 
 // 4-D tiled TMA load of one box into shared memory, completing on `bar` (tx bytes).

@@ -209,6 +209,47 @@ def test_attn_many_rows_and_long_row(sgd):
     check_attn(sgd, case, case.query(40, 8), 8, parent=tree(case.rng, 3, 40))
 
 
+def dense_attn64(case, q, G, parent=None, window=0, sinks=0):
+    """The oracle's formula in float64 torch on the GPU, for sizes that numpy loops are too slow for."""
+    B, M, Hq, D = q.shape
+    one = lambda x: 1.0 if x is None else float(np.float32(x))  # noqa: E731
+    k, v, q = case.k.cuda(), case.v.cuda(), q.cuda().double()
+    out, mass = torch.zeros(B, M, Hq, D, dtype=torch.float64), torch.zeros(B, M, Hq, D, dtype=torch.float64)
+    lse, zabs = torch.zeros(B, M, Hq, dtype=torch.float64), torch.zeros(B, M, Hq, dtype=torch.float64)
+    for b in range(B):
+        L = int(case.lens[b])
+        see = torch.from_numpy(orc.visible(L, M, M, None if parent is None else parent[b], window, sinks)).cuda()
+        pages = torch.from_numpy(case.table[b, :-(-L // PAGE)]).long().cuda()
+        for h in range(Hq // G):
+            kk = k[pages, h].reshape(-1, D)[:L].double() * one(case.ks)
+            vv = v[pages, h].reshape(-1, D)[:L].double() * one(case.vs)
+            qq = q[b, :, h * G:h * G + G]
+            z = (qq @ kk.T / D ** 0.5).masked_fill(~see[:, None], -float("inf"))
+            lse[b, :, h * G:h * G + G] = torch.logsumexp(z, -1)
+            p = torch.softmax(z, -1)
+            out[b, :, h * G:h * G + G], mass[b, :, h * G:h * G + G] = p @ vv, p @ vv.abs()
+            zabs[b, :, h * G:h * G + G] = (qq.abs() @ kk.abs().T / D ** 0.5).masked_fill(~see[:, None], 0).amax(-1)
+    return [t.numpy() for t in (out, lse, mass, zabs)]
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 64), ("int8", 128), ("int8", 64)])
+@pytest.mark.parametrize("M,G,window", [(16, 8, 0), (4, 8, 0), (3, 5, 900), (32, 8, 0), (24, 8, 1500)])
+def test_attn_many_tiles(sgd, dtype, D, M, G, window):
+    # a CTA walks many tiles and several segments with ragged ends, the memory pipeline full all along;
+    # run again and again, since a missing wait would show only now and then
+    rng = np.random.default_rng(D + M)
+    case = Case([int(x) for x in rng.integers(700, 9000, 20)], Hkv=4, D=D, dtype=dtype, seed=D)
+    q, par = case.query(M, G), tree(case.rng, 20, M)
+    ref = dense_attn64(case, q, G, par, window, 5)
+    cache, qc = case.gpu(sgd), q.cuda()
+    first = sgd.paged_attn(qc, G, cache, ints(par), window=window, sinks=5)
+    compare_attn(first[0], first[1], *ref)
+    for _ in range(20):
+        out, lse, ws = sgd.paged_attn(qc, G, cache, ints(par), window=window, sinks=5)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert sgd.workspace_status(ws) == 0
+
+
 def test_attn_repeats_bit_for_bit(sgd):
     case = Case((3000, 800, 5000, 20), seed=31)
     cache, q = case.gpu(sgd), case.query(8, 8).cuda()
