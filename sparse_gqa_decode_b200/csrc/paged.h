@@ -47,7 +47,7 @@ struct VerifyArgs {
     int64_t V;
     bool f32;
 };
-int launch_verify(const VerifyArgs &a, cudaStream_t s);
+int launch_verify(const VerifyArgs &a, int sms, cudaStream_t s);
 
 // sgd_paged_attn
 struct PagedAttnArgs {

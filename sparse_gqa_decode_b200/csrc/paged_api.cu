@@ -126,7 +126,7 @@ int sgd_verify_tree(const void *p, sgd_dtype p_dtype, const void *q, int B, int 
     a.n_path = n_path, a.path = path, a.next = next_token;
     a.status = status_of(workspace);
     a.B = B, a.M = M, a.V = V, a.f32 = p_dtype == SGD_F32;
-    return launch_verify(a, s);
+    return launch_verify(a, sms, s);
 }
 
 int sgd_pages_reserve(const sgd_paged_kv *kv, const int32_t *add, int32_t *new_lens, void *workspace,

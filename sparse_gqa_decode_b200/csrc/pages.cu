@@ -309,12 +309,13 @@ __global__ void __launch_bounds__(256) append_kernel(PagedView kv, const __nv_bf
 }
 
 // Compaction in place: of one row and KV head, entry base + list[i] moves to base + i, i < n.
-// list ascends strictly from >= 0, so list[i] >= i and a row is never overwritten before the
-// entries with smaller i, the only ones whose source it can be, were read: chunks of rows go in order,
-// each read whole, then (after a barrier) written.  The next chunk's sources are later rows than any
-// destination so far, so they may be read before this chunk is written.
+// list ascends strictly from >= 0, so list[i] >= i, and the row that entry i overwrites can only be the
+// source of entries up to i: steps of rows are written in order, each after a barrier behind which all
+// sources up to its own were read.  Reading ahead is always safe (a source is never a row that a smaller
+// entry overwrote), so the steps' sources stream through a ring of asynchronous copies, kRing - 1 steps
+// ahead (32 KB a CTA), and their list entries as far ahead of those.
 // CTA (row, KV head; K or V; slice of the row's bytes).
-constexpr int kCompactThreads = 256;
+constexpr int kCompactThreads = 256, kRing = 5, kPer = 2;  // kPer: 16-byte pieces of a thread per step
 
 template <bool ACCEPT>
 __global__ void __launch_bounds__(kCompactThreads) compact_kernel(PagedView kv, CompactArgs a) {
@@ -357,11 +358,13 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(PagedView kv, 
     if (threadIdx.x == 0 && h == 0 && blockIdx.y == 0 && blockIdx.z == 0) a.new_lens[b] = base + n;
 
     const int64_t row_bytes = (int64_t)kv.D * kv.es, page_bytes = (int64_t)kv.Hkv * SGD_PAGE * row_bytes;
-    const int lanes = a.slice / 16;                      // threads of a row's slice
-    const int rows = kCompactThreads / lanes;            // rows in one step of the block
+    const int lanes = a.slice / 16;                            // threads of a row's slice
+    const int per = kCompactThreads / lanes, rows = per * kPer;  // rows of a step: 64 or 128
     const int r0 = threadIdx.x / lanes;
     uint8_t *pool = static_cast<uint8_t *>(blockIdx.y ? kv.v : kv.k) + (int64_t)h * SGD_PAGE * row_bytes +
                     (int64_t)blockIdx.z * a.slice + (threadIdx.x % lanes) * 16;
+    __shared__ uint4 ring[kRing][kPer][kCompactThreads];  // a thread's pieces are its own
+    __shared__ int32_t ids[2 * kRing][kCompactThreads / 4 * kPer];
     auto at = [&](int t) -> uint8_t * {  // entry t's 16 bytes, NULL for a page outside the pool
         const int p = row[t / SGD_PAGE];
         if (p < 0 || p >= kv.n_pages) {
@@ -370,42 +373,54 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(PagedView kv, 
         }
         return pool + p * page_bytes + (t % SGD_PAGE) * row_bytes;
     };
-    constexpr int U = 8;  // 16-byte loads in flight per thread: 32 KB a CTA, beside the next chunk's
-    uint4 x[U];
-    uint8_t *to[U];
-    auto load = [&](int i0) {
-        int s[U];
+    auto load_ids = [&](int step) {
+        const int i = step * rows + threadIdx.x;
+        if ((int)threadIdx.x < rows && i < n) cp_async_4(&ids[step % (2 * kRing)][threadIdx.x], list + i);
+    };
+    // the entry that moves to i, clamped to [i, limit) so that a bad list stays within the row
+    auto source = [&](int step, int k) {
+        const int i = step * rows + k, id = ids[step % (2 * kRing)][k], s = min(max(id, i), limit - 1);
+        const int prev = i == 0 ? -1 : k > 0 ? ids[step % (2 * kRing)][k - 1] : ids[(step - 1) % (2 * kRing)][rows - 1];
+        if (s != id || prev >= id) bad |= SGD_STATUS_BAD_INDEX;
+        return s;
+    };
+    uint32_t moves = 0;  // bit kPer * (step % kRing) + u: the thread's piece u of that step moves
+    auto load = [&](int step) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * rows + r0;
-            to[u] = nullptr;
-            s[u] = i;
+        for (int u = 0; u < kPer; ++u) {
+            const int k = u * per + r0, i = step * rows + k, bit = kPer * (step % kRing) + u;
+            moves &= ~(1u << bit);
             if (i < n) {
-                const int k = list[i];
-                s[u] = min(max(k, i), limit - 1);
-                if (s[u] != k || (i > 0 && list[i - 1] >= k)) bad |= SGD_STATUS_BAD_INDEX;
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = i0 + u * rows + r0;
-            if (s[u] != i) {
-                const uint8_t *from = at(base + s[u]);
-                to[u] = at(base + i);
-                if (from && to[u]) x[u] = *reinterpret_cast<const uint4 *>(from);
-                else to[u] = nullptr;
+                const int s = source(step, k);
+                const uint8_t *from = s != i ? at(base + s) : nullptr;
+                if (from && at(base + i)) {
+                    cp_async_16(&ring[step % kRing][u][threadIdx.x], from);
+                    moves |= 1u << bit;
+                }
             }
         }
     };
-    const int chunk = rows * U;
-    load(0);
-    for (int i0 = 0; i0 < n; i0 += chunk) {
-        __syncthreads();  // every source of this chunk is in registers
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (to[u]) *reinterpret_cast<uint4 *>(to[u]) = x[u];
-        load(i0 + chunk);
+    const int steps = (n + rows - 1) / rows;
+    for (int s = 0; s < kRing - 1; ++s) load_ids(s);
+    cp_async_wait_all();
+    __syncthreads();
+    for (int s = 0; s < kRing - 1; ++s) {  // group s: the sources of step s, the list of step s + kRing - 1
+        load(s);
+        load_ids(s + kRing - 1);
+        cp_async_commit();
     }
+    for (int s = 0; s < steps; ++s) {
+        cp_async_wait_group<kRing - 2>();  // groups up to s
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kPer; ++u)
+            if (moves >> (kPer * (s % kRing) + u) & 1)
+                *reinterpret_cast<uint4 *>(at(base + s * rows + u * per + r0)) = ring[s % kRing][u][threadIdx.x];
+        load(s + kRing - 1);
+        load_ids(s + 2 * (kRing - 1));
+        cp_async_commit();
+    }
+    cp_async_wait_all();
     if (bad) atomicOr(a.status, bad);
 }
 
