@@ -24,7 +24,6 @@ struct CompactArgs {
     int64_t kept_total;
     int32_t *new_lens;
     int32_t *status;
-    int slice;  // bytes of a row that one CTA moves (set by the launch)
 };
 
 int launch_pages_reserve(const PagedView &kv, const int32_t *add, int32_t *new_lens, int32_t *scratch,

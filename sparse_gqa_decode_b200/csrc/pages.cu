@@ -312,13 +312,22 @@ __global__ void __launch_bounds__(256) append_kernel(PagedView kv, const __nv_bf
 // list ascends strictly from >= 0, so list[i] >= i, and the row that entry i overwrites can only be the
 // source of entries up to i: steps of rows are written in order, each after a barrier behind which all
 // sources up to its own were read.  Reading ahead is always safe (a source is never a row that a smaller
-// entry overwrote), so the steps' sources stream through a ring of asynchronous copies, kRing - 1 steps
-// ahead (32 KB a CTA), and their list entries as far ahead of those.
-// CTA (row, KV head; K or V; slice of the row's bytes).
-constexpr int kCompactThreads = 256, kRing = 5, kPer = 2;  // kPer: 16-byte pieces of a thread per step
+// entry overwrote), so the steps' sources stream through a ring of asynchronous copies, two steps of 32 KB
+// ahead, and their list entries as far ahead of those.  A step has a row for every thread, which finds where it
+// comes from and goes to; with fewer rows a step, or pieces looked up one by one, the lookups bound the kernel
+// (8 x 32K tokens kept to an eighth: 94 us piece by piece, 79 us with 64 rows a step).
+// CTA (row, KV head; K or V; slice of the row's bytes); LANES threads of 16 bytes to a slice.
+constexpr int kCompactThreads = 256, kRing = 3;
 
-template <bool ACCEPT>
-__global__ void __launch_bounds__(kCompactThreads) compact_kernel(PagedView kv, CompactArgs a) {
+template <int LANES>
+struct CompactShared {
+    uint4 ring[kRing][LANES][kCompactThreads];  // a thread's pieces are its own
+    int32_t ids[kRing + 2][kCompactThreads];    // list entries of the steps ahead
+    int2 move[kRing + 1][kCompactThreads];      // their (from, to) as rows of the pool; from < 0: stays
+};
+
+template <bool ACCEPT, int LANES>
+__global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(PagedView kv, CompactArgs a) {
     const int b = blockIdx.x / kv.Hkv, h = blockIdx.x % kv.Hkv;
     int L = kv.lens[b], bad = 0, n, base = 0, limit;
     const int32_t *list;
@@ -357,71 +366,92 @@ __global__ void __launch_bounds__(kCompactThreads) compact_kernel(PagedView kv, 
     }
     if (threadIdx.x == 0 && h == 0 && blockIdx.y == 0 && blockIdx.z == 0) a.new_lens[b] = base + n;
 
-    const int64_t row_bytes = (int64_t)kv.D * kv.es, page_bytes = (int64_t)kv.Hkv * SGD_PAGE * row_bytes;
-    const int lanes = a.slice / 16;                            // threads of a row's slice
-    const int per = kCompactThreads / lanes, rows = per * kPer;  // rows of a step: 64 or 128
-    const int r0 = threadIdx.x / lanes;
-    uint8_t *pool = static_cast<uint8_t *>(blockIdx.y ? kv.v : kv.k) + (int64_t)h * SGD_PAGE * row_bytes +
-                    (int64_t)blockIdx.z * a.slice + (threadIdx.x % lanes) * 16;
-    __shared__ uint4 ring[kRing][kPer][kCompactThreads];  // a thread's pieces are its own
-    __shared__ int32_t ids[2 * kRing][kCompactThreads / 4 * kPer];
-    auto at = [&](int t) -> uint8_t * {  // entry t's 16 bytes, NULL for a page outside the pool
-        const int p = row[t / SGD_PAGE];
-        if (p < 0 || p >= kv.n_pages) {
-            bad |= SGD_STATUS_BAD_INDEX;
-            return nullptr;
-        }
-        return pool + p * page_bytes + (t % SGD_PAGE) * row_bytes;
-    };
+    extern __shared__ __align__(16) uint8_t smem[];
+    auto &sh = *reinterpret_cast<CompactShared<LANES> *>(smem);
+    constexpr int ROWS = kCompactThreads;  // of a step
+    const int row_bytes = kv.D * kv.es, tid = threadIdx.x;
+    uint8_t *pool = static_cast<uint8_t *>(blockIdx.y ? kv.v : kv.k) + (int64_t)blockIdx.z * LANES * 16 + tid % LANES * 16;
+    auto row_of = [&](int u) { return u * (ROWS / LANES) + tid / LANES; };  // the step's row of the thread's piece u
     auto load_ids = [&](int step) {
-        const int i = step * rows + threadIdx.x;
-        if ((int)threadIdx.x < rows && i < n) cp_async_4(&ids[step % (2 * kRing)][threadIdx.x], list + i);
+        const int i = step * ROWS + tid;
+        if (i < n) cp_async_4(&sh.ids[step % (kRing + 2)][tid], list + i);
     };
-    // the entry that moves to i, clamped to [i, limit) so that a bad list stays within the row
-    auto source = [&](int step, int k) {
-        const int i = step * rows + k, id = ids[step % (2 * kRing)][k], s = min(max(id, i), limit - 1);
-        const int prev = i == 0 ? -1 : k > 0 ? ids[step % (2 * kRing)][k - 1] : ids[(step - 1) % (2 * kRing)][rows - 1];
-        if (s != id || prev >= id) bad |= SGD_STATUS_BAD_INDEX;
-        return s;
+    auto pool_row = [&](int t) {  // entry t, -1 for a page outside the pool
+        const int p = row[t / SGD_PAGE];
+        if (p >= 0 && p < kv.n_pages) return (p * kv.Hkv + h) * SGD_PAGE + t % SGD_PAGE;
+        bad |= SGD_STATUS_BAD_INDEX;
+        return -1;
     };
-    uint32_t moves = 0;  // bit kPer * (step % kRing) + u: the thread's piece u of that step moves
+    auto resolve = [&](int step) {  // thread k: the step's row k
+        const int i = step * ROWS + tid;
+        if (i >= n) return;
+        const int id = sh.ids[step % (kRing + 2)][tid];
+        const int prev = i == 0 ? -1 : tid > 0 ? sh.ids[step % (kRing + 2)][tid - 1] : sh.ids[(step - 1) % (kRing + 2)][ROWS - 1];
+        const int from = min(max(id, i), limit - 1);  // a bad list stays within [i, limit)
+        if (from != id || prev >= id) bad |= SGD_STATUS_BAD_INDEX;
+        int2 m = make_int2(-1, -1);
+        if (from != i) {
+            m = make_int2(pool_row(base + from), pool_row(base + i));
+            if (m.y < 0) m.x = -1;
+        }
+        sh.move[step % (kRing + 1)][tid] = m;
+    };
     auto load = [&](int step) {
 #pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-            const int k = u * per + r0, i = step * rows + k, bit = kPer * (step % kRing) + u;
-            moves &= ~(1u << bit);
-            if (i < n) {
-                const int s = source(step, k);
-                const uint8_t *from = s != i ? at(base + s) : nullptr;
-                if (from && at(base + i)) {
-                    cp_async_16(&ring[step % kRing][u][threadIdx.x], from);
-                    moves |= 1u << bit;
-                }
-            }
+        for (int u = 0; u < LANES; ++u) {
+            if (step * ROWS + row_of(u) >= n) continue;
+            const int from = sh.move[step % (kRing + 1)][row_of(u)].x;
+            if (from >= 0) cp_async_16(&sh.ring[step % kRing][u][tid], pool + (int64_t)from * row_bytes);
         }
     };
-    const int steps = (n + rows - 1) / rows;
-    for (int s = 0; s < kRing - 1; ++s) load_ids(s);
+    auto store = [&](int step) {
+#pragma unroll
+        for (int u = 0; u < LANES; ++u) {
+            if (step * ROWS + row_of(u) >= n) continue;
+            const int2 m = sh.move[step % (kRing + 1)][row_of(u)];
+            if (m.x >= 0) *reinterpret_cast<uint4 *>(pool + (int64_t)m.y * row_bytes) = sh.ring[step % kRing][u][tid];
+        }
+    };
+    constexpr int AHEAD = ACCEPT ? 1 : kRing;  // an accepted path is one step
+    for (int s = 0; s < AHEAD; ++s) load_ids(s);
     cp_async_wait_all();
     __syncthreads();
-    for (int s = 0; s < kRing - 1; ++s) {  // group s: the sources of step s, the list of step s + kRing - 1
-        load(s);
-        load_ids(s + kRing - 1);
-        cp_async_commit();
-    }
-    for (int s = 0; s < steps; ++s) {
-        cp_async_wait_group<kRing - 2>();  // groups up to s
+    for (int s = 0; s < AHEAD; ++s) resolve(s);
+    __syncthreads();
+    if constexpr (ACCEPT) {
+        load(0);
+        cp_async_wait_all();
         __syncthreads();
-#pragma unroll
-        for (int u = 0; u < kPer; ++u)
-            if (moves >> (kPer * (s % kRing) + u) & 1)
-                *reinterpret_cast<uint4 *>(at(base + s * rows + u * per + r0)) = ring[s % kRing][u][threadIdx.x];
-        load(s + kRing - 1);
-        load_ids(s + 2 * (kRing - 1));
-        cp_async_commit();
+        store(0);
+    } else {
+        const int steps = (n + ROWS - 1) / ROWS;
+        for (int s = 0; s < kRing - 1; ++s) {  // group s: the sources of step s, the list of step s + kRing
+            load(s);
+            load_ids(s + kRing);
+            cp_async_commit();
+        }
+        for (int s = 0; s < steps; ++s) {
+            cp_async_wait_group<kRing - 2>();  // groups up to s
+            __syncthreads();
+            store(s);
+            load(s + kRing - 1);
+            load_ids(s + 2 * kRing - 1);
+            cp_async_commit();
+            resolve(s + kRing);
+        }
+        cp_async_wait_all();
     }
-    cp_async_wait_all();
     if (bad) atomicOr(a.status, bad);
+}
+
+template <bool ACCEPT, int LANES>
+int launch_compact(const PagedView &kv, const CompactArgs &a, cudaStream_t s) {
+    auto k = compact_kernel<ACCEPT, LANES>;
+    constexpr int smem = sizeof(CompactShared<LANES>);
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return SGD_ERR_CUDA;
+    const dim3 grid(kv.B * kv.Hkv, 2, kv.D * kv.es / (LANES * 16));
+    const cudaError_t e = launch_k(k, grid, dim3(kCompactThreads), smem, s, 1, kv, a);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? SGD_OK : SGD_ERR_CUDA;
 }
 
 bool ok() { return cudaGetLastError() == cudaSuccess; }
@@ -456,13 +486,9 @@ int launch_pages_append(const PagedView &kv, const void *k_new, const void *v_ne
     return ok() ? SGD_OK : SGD_ERR_CUDA;
 }
 
-int launch_pages_compact(const PagedView &kv, const CompactArgs &args, bool accept, cudaStream_t s) {
-    CompactArgs a = args;
-    const int row_bytes = kv.D * kv.es;
-    a.slice = row_bytes < 128 ? row_bytes : 128;
-    const dim3 grid(kv.B * kv.Hkv, 2, row_bytes / a.slice);
-    launch_k(accept ? compact_kernel<true> : compact_kernel<false>, grid, dim3(kCompactThreads), 0, s, 1, kv, a);
-    return ok() ? SGD_OK : SGD_ERR_CUDA;
+int launch_pages_compact(const PagedView &kv, const CompactArgs &a, bool accept, cudaStream_t s) {
+    if (kv.D * kv.es < 128) return accept ? launch_compact<true, 4>(kv, a, s) : launch_compact<false, 4>(kv, a, s);
+    return accept ? launch_compact<true, 8>(kv, a, s) : launch_compact<false, 8>(kv, a, s);
 }
 
 }  // namespace sgd
