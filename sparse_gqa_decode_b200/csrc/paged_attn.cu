@@ -113,10 +113,11 @@ struct Cfg {
     static constexpr bool I8 = I8_, TWO = TWO_;
     static constexpr int HALVES = D / 64;                 // 64-channel halves, 16 KB each of a tile
     static constexpr int TILE_BYTES = kTile * D * 2;
-    static constexpr int Q_BUFS = 2;                      // TWO: the two row tiles; else two segments'
-    static constexpr int Q_STAGES = TWO ? 1 : 2;
-    static constexpr int SLOTS = I8 ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 8);  // bf16 tiles of K or V
-    static constexpr int RAW = I8 ? (D == 128 ? 4 : 8) : 0;                     // code tiles in flight
+    // Q: the two row tiles, or two segments'; one segment's with codes, whose tiles in flight need the space (64 KB
+    // of codes in flight, released only once widened, hold a third of HBM's rate back)
+    static constexpr int Q_STAGES = TWO || I8 ? 1 : 2, Q_BUFS = TWO ? 2 : Q_STAGES;
+    static constexpr int SLOTS = I8 ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 8);  // 16-bit tiles of K or V
+    static constexpr int RAW = !I8 ? 0 : D == 128 ? (TWO ? 4 : 6) : (TWO ? 8 : 12);  // code tiles in flight
     static constexpr int RAW_BYTES = kTile * D;
     static constexpr int CONVERT = I8 ? 128 : 0;         // threads that widen codes
     static constexpr int THREADS = 384 + CONVERT;
@@ -134,7 +135,7 @@ struct Cfg {
 
 struct Bars {
     uint64_t full[8], empty[8];          // ring of bf16 K / V tiles, in the order the products take them
-    uint64_t raw_full[8], raw_empty[8];  // I8: ring of code tiles
+    uint64_t raw_full[12], raw_empty[12];  // I8: ring of code tiles
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2], v_here[2], p_full[2], o_full[2];
     uint64_t q_ready, o_free, ml_full, drained;
@@ -381,100 +382,105 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
     } else if (warp == kWarpMma) {
         // ------------------------------------------------------------------ products
-        // One thread issues all products.  It waits for every KV tile, in ring order: a parity tells a barrier's
-        // phases apart only for a thread that misses none.  A wait costs a few hundred cycles here even where its
-        // barrier is done (the tensor cores' operand reads fill the shared memory's time), so a tile's V, and with two
-        // row tiles the next K, is waited for before its P, while the softmax is at work: 318 -> 264 us for 512 rows
-        // and 4 x 31K tokens.  An issuing warp for each group instead took 320 us.
-        if (lane == 0) {
-            constexpr uint32_t ID_QK = tc_idesc(C::I8, 128, kTile, false), ID_PV = tc_idesc(C::I8, 128, D, true);
-            const uint32_t sq = smem_u32(smem + C::OFF_Q), ss = smem_u32(smem + C::OFF_SLOT);
-            uint32_t at = 0, seg = 0, np[2] = {0, 0};
-            bool go = true;
-            auto slot = [&](uint32_t pos) { return ss + (pos % C::SLOTS) * C::TILE_BYTES; };
-            auto full = [&](uint32_t pos) { return go && (go = wait(&bar.full[pos % C::SLOTS], (pos / C::SLOTS) & 1)); };
-            auto release = [&](uint32_t pos) { tc_commit(&bar.empty[pos % C::SLOTS]); };
-            auto qk = [&](int g, uint32_t q, uint32_t pos) {  // S_g = Q K^T
-                tc_fence_after();
-                const uint64_t dq = desc_k_major(q), dk = desc_k_major(slot(pos));
+        // One thread issues all products, from code that the whole warp runs (the operands then stay in uniform
+        // registers; from a branch of one lane a product took 60 cycles to issue).  The warp waits for every KV tile, in
+        // ring order: a parity tells a barrier's phases apart only for who misses none.  A tile's V, and with two row
+        // tiles the next K, is waited for before its P, while the softmax is at work: 318 -> 264 us for 512 rows and
+        // 4 x 31K tokens.  An issuing warp for each group instead took 320 us.
+        constexpr uint32_t ID_QK = tc_idesc(C::I8, 128, kTile, false), ID_PV = tc_idesc(C::I8, 128, D, true);
+        const uint32_t sq = smem_u32(smem + C::OFF_Q), ss = smem_u32(smem + C::OFF_SLOT);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        uint32_t at = 0, seg = 0, np[2] = {0, 0};
+        bool go = true;
+        auto slot = [&](uint32_t pos) { return ss + (pos % C::SLOTS) * C::TILE_BYTES; };
+        auto full = [&](uint32_t pos) { return go && (go = wait_warp(&bar.full[pos % C::SLOTS], (pos / C::SLOTS) & 1)); };
+        auto commit = [&](uint64_t *m) {
+            if (elect_one()) tc_commit(m);
+        };
+        auto release = [&](uint32_t pos) { commit(&bar.empty[pos % C::SLOTS]); };
+        auto qk = [&](int g, uint32_t q, uint32_t pos) {  // S_g = Q K^T
+            tc_fence_after();
+            const uint64_t dq = desc_k_major(q), dk = desc_k_major(slot(pos));
+            if (elect_one()) {
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) {
                     const uint32_t off = ((j / 4) * (kTile * 128) + (j % 4) * 32) >> 4;  // in the descriptors' 16 bytes
-                    mma_ss(tmem + g * 128, dq + off, dk + off, ID_QK, j > 0);
+                    mma_ss(tm + g * 128, dq + off, dk + off, ID_QK, j > 0);
                 }
                 tc_commit(&bar.s_full[g]);
-            };
-            auto pv = [&](int g, uint32_t pos, bool acc) {  // O_g (+)= P_g V
-                if (!go || !(go = wait(&bar.p_full[g], np[g]++ & 1))) return false;
-                tc_fence_after();
-                const uint64_t dv = desc_mn_major(slot(pos), kTile * 128);
+            }
+        };
+        auto pv = [&](int g, uint32_t pos, bool acc) {  // O_g (+)= P_g V
+            if (!go || !(go = wait_warp(&bar.p_full[g], np[g]++ & 1))) return false;
+            tc_fence_after();
+            const uint64_t dv = desc_mn_major(slot(pos), kTile * 128);
+            if (elect_one()) {
 #pragma unroll
                 for (int j = 0; j < kTile / 16; ++j)
-                    mma_ts(tmem + 256 + g * 128, tmem + g * 128 + j * 8, dv + j * (2048 >> 4), ID_PV, acc || j > 0);
-                return true;
-            };
-            while (go && w.next(kv, a)) {
-                const int T = w.hi - w.lo, qs = seg % C::Q_STAGES;
-                go = C::I8 ? wait(&bar.q_ready, seg & 1) : wait(&bar.q_full[qs], (seg / C::Q_STAGES) & 1);
+                    mma_ts(tm + 256 + g * 128, tm + g * 128 + j * 8, dv + j * (2048 >> 4), ID_PV, acc || j > 0);
+            }
+            return true;
+        };
+        while (go && w.next(kv, a)) {
+            const int T = __shfl_sync(0xffffffffu, w.hi - w.lo, 0), qs = seg % C::Q_STAGES;
+            go = C::I8 ? wait_warp(&bar.q_ready, seg & 1) : wait_warp(&bar.q_full[qs], (seg / C::Q_STAGES) & 1);
+            if (!go) break;
+            const uint32_t q0 = sq + (C::TWO ? 0 : qs) * C::TILE_BYTES;
+            if constexpr (C::TWO) {
+                if (!full(at)) break;
+                for (int g = 0; g < 2; ++g) qk(g, q0 + g * C::TILE_BYTES, at);
+                release(at);
+                if (T == 1) commit(&bar.q_empty[qs]);  // the last product that reads Q was issued
+            } else {
+                for (int g = 0; g < min(T, 2); ++g) {
+                    if (!full(at + g)) break;
+                    qk(g, q0, at + g);
+                    release(at + g);
+                }
                 if (!go) break;
-                const uint32_t q0 = sq + (C::TWO ? 0 : qs) * C::TILE_BYTES;
+                if (T <= 2) commit(&bar.q_empty[qs]);
+            }
+            if (seg > 0 && !(go = wait_warp(&bar.o_free, (seg - 1) & 1))) break;  // the last segment's O was read
+            for (int j = 0; j < T; ++j) {
+                const uint32_t v_at = at + pos_v<C::TWO>(j, T), k_at = at + pos_k<C::TWO>(C::TWO ? j + 1 : j + 2);
+                if (!full(v_at)) break;
+                if (lane == 0 && has_unseen(w.s, a, tile_of(w.s, w.lo + j) * kTile)) {  // its rows may be cleared
+                    mbar_arrive(&bar.v_here[C::TWO ? 0 : j & 1]);
+                    if (C::TWO) mbar_arrive(&bar.v_here[1]);
+                }
+                __syncwarp();
                 if constexpr (C::TWO) {
-                    if (!full(at)) break;
-                    for (int g = 0; g < 2; ++g) qk(g, q0 + g * C::TILE_BYTES, at);
-                    release(at);
-                    if (T == 1) tc_commit(&bar.q_empty[qs]);  // the last product that reads Q was issued
-                } else {
-                    for (int g = 0; g < min(T, 2); ++g) {
-                        if (!full(at + g)) break;
-                        qk(g, q0, at + g);
-                        release(at + g);
+                    const bool more = j + 1 < T;
+                    if (more && !full(k_at)) break;
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        if (!pv(g, v_at, j > 0)) break;
+                        if (more) qk(g, q0 + g * C::TILE_BYTES, k_at);
+                        else commit(&bar.o_full[g]);
                     }
                     if (!go) break;
-                    if (T <= 2) tc_commit(&bar.q_empty[qs]);
-                }
-                if (seg > 0 && !(go = wait(&bar.o_free, (seg - 1) & 1))) break;  // the last segment's O was read
-                for (int j = 0; j < T; ++j) {
-                    const uint32_t v_at = at + pos_v<C::TWO>(j, T), k_at = at + pos_k<C::TWO>(C::TWO ? j + 1 : j + 2);
-                    const bool unseen = has_unseen(w.s, a, tile_of(w.s, w.lo + j) * kTile);
-                    if (!full(v_at)) break;
-                    if constexpr (C::TWO) {
-                        const bool more = j + 1 < T;
-                        if (unseen) {  // the softmax warps may clear its rows
-                            mbar_arrive(&bar.v_here[0]);
-                            mbar_arrive(&bar.v_here[1]);
-                        }
-                        if (more && !full(k_at)) break;
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            if (!pv(g, v_at, j > 0)) break;
-                            if (more) qk(g, q0 + g * C::TILE_BYTES, k_at);
-                            else tc_commit(&bar.o_full[g]);
-                        }
-                        if (!go) break;
-                        release(v_at);
-                        if (more) release(k_at);
-                        if (j + 2 == T) tc_commit(&bar.q_empty[qs]);
-                    } else {
-                        const int g = j & 1;
-                        if (unseen) mbar_arrive(&bar.v_here[g]);
-                        if (!pv(g, v_at, j > 1)) break;
-                        if (j + 2 >= T) tc_commit(&bar.o_full[g]);
-                        release(v_at);
-                        if (j + 2 < T) {
-                            if (!full(k_at)) break;
-                            qk(g, q0, k_at);
-                            release(k_at);
-                            if (j + 3 == T) tc_commit(&bar.q_empty[qs]);
-                        }
+                    release(v_at);
+                    if (more) release(k_at);
+                    if (j + 2 == T) commit(&bar.q_empty[qs]);
+                } else {
+                    const int g = j & 1;
+                    if (!pv(g, v_at, j > 1)) break;
+                    if (j + 2 >= T) commit(&bar.o_full[g]);
+                    release(v_at);
+                    if (j + 2 < T) {
+                        if (!full(k_at)) break;
+                        qk(g, q0, k_at);
+                        release(k_at);
+                        if (j + 3 == T) commit(&bar.q_empty[qs]);
                     }
                 }
-                at += 2 * T;
-                ++seg;
             }
-            // no product may still be reading, and no arrival be due, when the CTA ends
-            tc_commit(&bar.drained);
-            mbar_drain(&bar.drained, 0, a.wait_limit);
+            at += 2 * T;
+            ++seg;
         }
+        // no product may still be reading, and no arrival be due, when the CTA ends
+        commit(&bar.drained);
+        if (lane == 0) mbar_drain(&bar.drained, 0, a.wait_limit);
     } else if (warp >= kWarpSoftmax && warp < kWarpSoftmax + 8) {
         // ------------------------------------------------------------------ softmax
         const int g = (warp - kWarpSoftmax) >> 2, wq = warp & 3;
@@ -769,52 +775,55 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
     } else if (C::I8 && warp >= kWarpConvert) {
         // ------------------------------------------------------------------ codes to f16
+        constexpr int UNITS = kTile * D / 16, U = UNITS / 128, RAW = C::RAW > 0 ? C::RAW : 1;  // 16 codes each
         const int ct = tid - kWarpConvert * 32;
-        uint32_t at = 0;
+        uint32_t at = 0, rd = 0, end = 0;  // ring positions written, read, known so far
         bool go = true;
-        while (go && w.next(kv, a)) {
-            const int T = w.hi - w.lo;
-            for (int i = 0; i < 2 * T; ++i, ++at) {
-                constexpr int RAW = C::RAW > 0 ? C::RAW : 1;
-                const int rs = at % RAW, bs = at % C::SLOTS;
-                if (!(go = wait_warp(&bar.raw_full[rs], (at / RAW) & 1))) break;
-                if (at >= C::SLOTS && !(go = wait_warp(&bar.empty[bs], (at / C::SLOTS - 1) & 1))) break;
-                const uint8_t *src = smem + C::OFF_RAW + rs * C::RAW_BYTES;
-                uint8_t *dst = smem + C::OFF_SLOT + bs * C::TILE_BYTES;
-                constexpr int UNITS = kTile * D / 16, U = 4;  // 16 codes each; U loads of a thread in flight
-#pragma unroll 1
-                for (int u0 = ct; u0 < UNITS; u0 += 128 * U) {
-                    uint4 x[U];
+        auto known = [&](uint32_t pos) {  // whether the CTA's range has this position
+            while (pos >= end && w.next(kv, a)) end += 2 * (w.hi - w.lo);
+            return pos < end;
+        };
+        auto read = [&](uint4 (&x)[U]) {
+            if (!go || !known(rd)) return;
+            const int rs = rd % RAW;
+            if (!(go = wait_warp(&bar.raw_full[rs], (rd / RAW) & 1))) return;
+            const uint8_t *src = smem + C::OFF_RAW + rs * C::RAW_BYTES;
 #pragma unroll
-                    for (int i = 0; i < U; ++i) x[i] = *reinterpret_cast<const uint4 *>(src + (u0 + 128 * i) * 16);
+            for (int i = 0; i < U; ++i) x[i] = lds128(smem_u32(src + (ct + 128 * i) * 16));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.raw_empty[rs]);
+            ++rd;
+        };
+        auto write = [&](const uint4 (&x)[U]) {
+            const int bs = at % C::SLOTS;
+            if (at >= C::SLOTS && !(go = wait_warp(&bar.empty[bs], (at / C::SLOTS - 1) & 1))) return;
+            uint8_t *dst = smem + C::OFF_SLOT + bs * C::TILE_BYTES;
 #pragma unroll
-                    for (int i = 0; i < U; ++i) {
-                        const int u = u0 + 128 * i, row = u / (D / 16), cb = u % (D / 16);
-                        uint32_t y[8];
-                        s8x4_to_f16x2x2(x[i].x, y[0], y[1]);
-                        s8x4_to_f16x2x2(x[i].y, y[2], y[3]);
-                        s8x4_to_f16x2x2(x[i].z, y[4], y[5]);
-                        s8x4_to_f16x2x2(x[i].w, y[6], y[7]);
-                        // two 16-byte pieces of the swizzled row; the second half's threads start with the odd one, so
-                        // that a quarter warp's stores cover all banks
-                        uint8_t *base = dst + (cb / 4) * (kTile * 128) + row * 128;
-                        const int ch = (cb % 4) * 2, odd = cb / 4 & 1;
+            for (int i = 0; i < U; ++i) {
+                const int u = ct + 128 * i, row = u / (D / 16), cb = u % (D / 16);
+                uint32_t y[8];
+                s8x4_to_f16x2x2(x[i].x, y[0], y[1]);
+                s8x4_to_f16x2x2(x[i].y, y[2], y[3]);
+                s8x4_to_f16x2x2(x[i].z, y[4], y[5]);
+                s8x4_to_f16x2x2(x[i].w, y[6], y[7]);
+                // two 16-byte pieces of the swizzled row; the second half's threads start with the odd one, so that a
+                // quarter warp's stores cover all banks
+                uint8_t *base = dst + (cb / 4) * (kTile * 128) + row * 128;
+                const int ch = (cb % 4) * 2, odd = cb / 4 & 1;
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int e = k ^ odd;
-                            *reinterpret_cast<uint4 *>(base + (((ch + e) ^ (row & 7)) * 16)) =
-                                e ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
-                        }
-                    }
-                }
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&bar.full[bs]);
-                    mbar_arrive(&bar.raw_empty[rs]);
+                for (int k = 0; k < 2; ++k) {
+                    const int e = k ^ odd;
+                    *reinterpret_cast<uint4 *>(base + (((ch + e) ^ (row & 7)) * 16)) =
+                        e ? make_uint4(y[4], y[5], y[6], y[7]) : make_uint4(y[0], y[1], y[2], y[3]);
                 }
             }
-        }
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.full[bs]);
+            ++at;
+        };
+        uint4 x[U];
+        for (read(x); go && at < end; read(x)) write(x);
     }
     __syncwarp();
     tc_fence_before();

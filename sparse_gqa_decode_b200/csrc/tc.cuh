@@ -91,6 +91,18 @@ constexpr uint32_t tc_idesc(bool f16, int M, int N, bool b_mn_major) {
            (uint32_t)(M >> 4) << 24;
 }
 
+// True in one lane of a converged warp, the same one each time.  Products and commits are issued under it from
+// code that the whole warp runs: their operands then stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // D (tensor memory) (+)= A B; issued by one thread, executed in issue order
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
     asm volatile(
