@@ -92,7 +92,7 @@ int sgd_paged_attn(const void *q, int G, int M, const sgd_paged_kv *kv, const in
         return SGD_ERR_ALIGN;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     PagedAttnArgs a = {};
-    rc = begin(workspace, workspace_bytes, workspace_bytes_of(kv, G, M), true, s, &a.sms);
+    rc = begin(workspace, workspace_bytes, workspace_bytes_of(kv, G, M), false, s, &a.sms);
     if (rc != SGD_OK) return rc;
     a.q = q, a.parent = parent, a.n_nodes = n_nodes, a.out = out, a.lse = lse;
     // no position reaches 2^30 (max_pages < 2^24): larger values mean the same

@@ -58,6 +58,8 @@ struct AttnPlan {
     float *o_part;     // [grid * 2, rows of a CTA, D] partial outputs, normalised
     float *lse_part;   // [grid * 2, rows of a CTA], log2 units
     int2 *item;        // [B * Hkv] first and last range of each item
+    int32_t *status;   // [grid] the CTAs' status bits
+    int n_cta;         // grid
 };
 
 // A row of the page table in a launch.
@@ -91,10 +93,29 @@ __device__ __forceinline__ Seq seq_of(const PagedView &kv, const PagedAttnArgs &
     return s;
 }
 
-// Whether the tile at t0 has entries that no query of the sequence sees (behind its end, or between the first tokens
-// and the windows): they may hold anything, so that their V rows have to become 0 before the product.
-__device__ __forceinline__ bool has_unseen(const Seq &s, const PagedAttnArgs &a, int t0) {
-    return t0 + kTile > s.L || (a.window && t0 < s.base + 1 - a.window && t0 + kTile > a.sinks);
+// The tile at t0 may have entries that no query of the sequence sees: behind its end, or between the first tokens and the
+// windows.  They may hold anything.  The second product runs over the 16-token steps [from, to) that hold
+// every seen entry; where those hold unseen ones too, their V rows have to become 0 before it.
+struct Steps {
+    int from, to;
+    bool unseen;
+};
+__device__ __forceinline__ Steps steps_of(const Seq &s, const PagedAttnArgs &a, int t0) {
+    int lo = 0, hi = min(max(s.L - t0, 0), kTile);
+    bool gap = false;
+    if (a.window) {
+        const int w = s.base + 1 - a.window - t0, f = a.sinks - t0;  // the windows' first entry, the end of the first tokens
+        if (w > 0 && w > f) {
+            if (f <= 0) lo = min(w, hi);
+            else if (w >= hi) hi = min(hi, f);
+            else gap = true;
+        }
+    }
+    Steps r;
+    r.to = max((hi + 15) / 16, 1);
+    r.from = min(lo / 16, r.to - 1);
+    r.unseen = gap || hi < r.to * 16 || lo > r.from * 16;
+    return r;
 }
 
 __device__ __forceinline__ int tile_of(const Seq &s, int v) { return v < s.sink_tiles ? v : v - s.sink_tiles + s.first; }
@@ -142,6 +163,7 @@ struct Bars {
     uint32_t tmem;
     int32_t abort;
     int32_t start_b, start_pos;          // the range's first row and its stream position
+    int32_t status;                      // the CTA's SGD_STATUS_* bits
 };
 static_assert(sizeof(Bars) <= 512, "barriers fit their space");
 
@@ -270,7 +292,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         prefetch_tensormap(&map_k);
         prefetch_tensormap(&map_v);
     }
+    if (tid == 32) bar.status = 0;
     if (warp == kWarpMma) tmem_alloc(&bar.tmem, 512);
+    __syncthreads();
 
     // the stream's length, this range of it, and the row it starts in: thread t sums consecutive rows
     int x0, x1;
@@ -279,7 +303,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int b0 = min(tid * per, kv.B), b1 = min(b0 + per, kv.B);
         int sum = 0, bad = 0;
         for (int b = b0; b < b1; ++b) sum += (seq_of(kv, a, b, bad).tiles + kItemCharge) * kv.Hkv;
-        if (bad && blockIdx.x == 0) atomicOr(a.status, bad);
+        if (bad && blockIdx.x == 0) atomicOr(&bar.status, bad);
         int total;
         int pos = block_exclusive_scan(sum, total, reinterpret_cast<int32_t *>(smem + C::OFF_ML));
         const int S = (total + plan.n_ranges - 1) / plan.n_ranges;
@@ -305,7 +329,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // the first poll looks at nothing but the barrier: while the tensor cores read their operands a shared-memory
     // access takes a few hundred cycles, and the abort flag would double that
     auto wait = [&](uint64_t *m, uint32_t parity) {
-        return mbar_try_wait(m, parity) || mbar_wait(m, parity, a.status, abort, a.wait_limit);
+        return mbar_try_wait(m, parity) || mbar_wait(m, parity, &bar.status, abort, a.wait_limit);
     };
     // the same answer in every lane, so that the warp stays together
     auto wait_warp = [&](uint64_t *m, uint32_t parity) { return (bool)__all_sync(0xffffffffu, wait(m, parity)); };
@@ -373,7 +397,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     }
                 }
             }
-            if (bad) atomicOr(a.status, bad);
+            if (bad) atomicOr(&bar.status, bad);
             if (*abort) {  // no copy may still be writing when the CTA ends
                 for (uint32_t i = at > N ? at - N : 0; i < at; ++i) mbar_drain(&full[i % N], (i / N) & 1, a.wait_limit);
                 for (uint32_t i = seg > C::Q_STAGES ? seg - C::Q_STAGES : 0; i < seg; ++i)
@@ -410,14 +434,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 tc_commit(&bar.s_full[g]);
             }
         };
-        auto pv = [&](int g, uint32_t pos, bool acc) {  // O_g (+)= P_g V
+        auto pv = [&](int g, uint32_t pos, const Steps &st, bool acc) {  // O_g (+)= P_g V
             if (!go || !(go = wait_warp(&bar.p_full[g], np[g]++ & 1))) return false;
             tc_fence_after();
             const uint64_t dv = desc_mn_major(slot(pos), kTile * 128);
             if (elect_one()) {
 #pragma unroll
                 for (int j = 0; j < kTile / 16; ++j)
-                    mma_ts(tm + 256 + g * 128, tm + g * 128 + j * 8, dv + j * (2048 >> 4), ID_PV, acc || j > 0);
+                    if (j >= st.from && j < st.to)
+                        mma_ts(tm + 256 + g * 128, tm + g * 128 + j * 8, dv + j * (2048 >> 4), ID_PV, acc || j > st.from);
             }
             return true;
         };
@@ -443,8 +468,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (seg > 0 && !(go = wait_warp(&bar.o_free, (seg - 1) & 1))) break;  // the last segment's O was read
             for (int j = 0; j < T; ++j) {
                 const uint32_t v_at = at + pos_v<C::TWO>(j, T), k_at = at + pos_k<C::TWO>(C::TWO ? j + 1 : j + 2);
+                const Steps st = steps_of(w.s, a, tile_of(w.s, w.lo + j) * kTile);
                 if (!full(v_at)) break;
-                if (lane == 0 && has_unseen(w.s, a, tile_of(w.s, w.lo + j) * kTile)) {  // its rows may be cleared
+                if (lane == 0 && st.unseen) {  // its rows may be cleared
                     mbar_arrive(&bar.v_here[C::TWO ? 0 : j & 1]);
                     if (C::TWO) mbar_arrive(&bar.v_here[1]);
                 }
@@ -454,7 +480,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     if (more && !full(k_at)) break;
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
-                        if (!pv(g, v_at, j > 0)) break;
+                        if (!pv(g, v_at, st, j > 0)) break;
                         if (more) qk(g, q0 + g * C::TILE_BYTES, k_at);
                         else commit(&bar.o_full[g]);
                     }
@@ -464,7 +490,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     if (j + 2 == T) commit(&bar.q_empty[qs]);
                 } else {
                     const int g = j & 1;
-                    if (!pv(g, v_at, j > 1)) break;
+                    if (!pv(g, v_at, st, j > 1)) break;
                     if (j + 2 >= T) commit(&bar.o_full[g]);
                     release(v_at);
                     if (j + 2 < T) {
@@ -494,8 +520,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             float scale = a.scale_log2, vs = 1.f, scale_k = scale;
             if constexpr (C::I8) {
                 const bool report = blockIdx.x == 0 && g == 0 && r == 0;
-                scale_k *= calibrated_scale(kv.k_scale, a.status, report);
-                vs = calibrated_scale(kv.v_scale, a.status, report);
+                scale_k *= calibrated_scale(kv.k_scale, &bar.status, report);
+                vs = calibrated_scale(kv.v_scale, &bar.status, report);
             }
             uint32_t at = 0, seg = 0, ns = 0, nv = 0, no[2] = {0, 0};
             float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);
@@ -534,7 +560,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                     if (s.base + j >= 0 && s.base + d < a.sinks) sees |= 1ull << j;
                             }
                         }
-                        if (bad) atomicOr(a.status, bad);
+                        if (bad) atomicOr(&bar.status, bad);
                     }
                 }
                 if constexpr (C::I8) {  // the row of Q as f16, scaled by 2^-e
@@ -674,19 +700,20 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         }
                         l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
                     }
-                    if (has_unseen(s, a, t0)) {  // clear V's rows once they are here
+                    const Steps st = steps_of(s, a, t0);
+                    if (st.unseen) {  // clear V's rows once they are here
                         if (!(go = wait_warp(&bar.v_here[g], nv++ & 1))) break;
                         const uint32_t pos = at + pos_v<C::TWO>(j, T);
                         uint8_t *v = smem + C::OFF_SLOT + (pos % C::SLOTS) * C::TILE_BYTES;
                         auto zero = [&](int from, int to) {  // rows of the tile, 16 bytes a lane
                             constexpr int PER = D / 8;
-                            from = max(from, 0), to = min(to, kTile);
+                            from = max(from, st.from * 16), to = min(to, st.to * 16);
                             for (int u = from * PER + wq * 32 + lane; u < to * PER; u += na * 32)
                                 *reinterpret_cast<uint4 *>(v + (u % PER) / 8 * kTile * 128 + u / PER * 128 + u % 8 * 16) =
                                     make_uint4(0, 0, 0, 0);
                         };
                         zero(s.L - t0, kTile);
-                        if (a.window) zero(a.sinks - t0, min(v_lo, s.L) - t0);
+                        if (a.window) zero(a.sinks - t0, v_lo - t0);
                         fence_proxy_async_shared();
                     }
                     tmem_wait_st();
@@ -828,6 +855,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (tid == 0) plan.status[blockIdx.x] = bar.status;
     if (warp == kWarpMma) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -844,6 +872,12 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(PagedView kv
     constexpr int ROWS = kMergeThreads / 32 / WARPS;  // output rows of a CTA
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wr = warp % WARPS;
     const int Hq = kv.Hkv * a.G;
+    if (blockIdx.x == 0 && warp == 0) {  // the call's status
+        int bits = 0;
+        for (int c = lane; c < plan.n_cta; c += 32) bits |= plan.status[c];
+        bits = __reduce_or_sync(0xffffffffu, (unsigned)bits);
+        if (lane == 0) *a.status = bits;
+    }
     const int64_t out_row = (int64_t)blockIdx.x * ROWS + warp / WARPS;
     if (out_row >= n_rows) return;  // WARPS > 1: ROWS is 1, the CTA leaves as a whole
     const int hq = (int)(out_row % Hq), m = (int)(out_row / Hq % a.M), b = (int)(out_row / Hq / a.M);
@@ -988,7 +1022,7 @@ int launch(const PagedView &kv, const PagedAttnArgs &a, const AttnPlan &plan, cu
 size_t paged_attn_scratch(int B, int Hkv, int D, int G, int M, int sms) {
     const Shape sh(G, M);
     const size_t slots = (size_t)sh.ranges(sms) * sh.RT * 2 * sh.rows();
-    return up256(slots * D * 4) + up256(slots * 4) + up256((size_t)B * Hkv * 8);
+    return up256(slots * D * 4) + up256(slots * 4) + up256((size_t)B * Hkv * 8) + up256((size_t)sms * 4);
 }
 
 int launch_paged_attn(const PagedView &kv, const PagedAttnArgs &a, cudaStream_t s) {
@@ -1006,6 +1040,8 @@ int launch_paged_attn(const PagedView &kv, const PagedAttnArgs &a, cudaStream_t 
     plan.o_part = reinterpret_cast<float *>(a.ws);
     plan.lse_part = reinterpret_cast<float *>(a.ws + up256(slots * kv.D * 4));
     plan.item = reinterpret_cast<int2 *>(a.ws + up256(slots * kv.D * 4) + up256(slots * 4));
+    plan.status = reinterpret_cast<int32_t *>(reinterpret_cast<uint8_t *>(plan.item) + up256((size_t)kv.B * kv.Hkv * 8));
+    plan.n_cta = plan.n_ranges * plan.RT;
     if (kv.es == 1) {
         if (kv.D == 128) return sh.two ? launch<Cfg<128, true, true>>(kv, a, plan, s) : launch<Cfg<128, true, false>>(kv, a, plan, s);
         return sh.two ? launch<Cfg<64, true, true>>(kv, a, plan, s) : launch<Cfg<64, true, false>>(kv, a, plan, s);
