@@ -173,7 +173,7 @@ void apply_test_hooks(DecodeArgs &a) {
 }
 
 void paged_test_hooks(long long *wait_limit, int *idle_producer) {
-    *wait_limit = g_hooks.wait_limit > 0 ? g_hooks.wait_limit : kWaitLimit;
+    *wait_limit = g_hooks.wait_limit > 0 ? g_hooks.wait_limit : kPagedWaitLimit;
     *idle_producer = g_hooks.idle_producer;
 }
 

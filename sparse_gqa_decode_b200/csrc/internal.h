@@ -113,6 +113,9 @@ int launch_gather_read(const void *a, const void *b, int64_t row_bytes, const in
 // host state shared with the paged entry points (api.cu): the current device's SM count (an SGD_ERR_*
 // code where it is not sm_100) and the pipeline test hooks
 int device_sms(int *sms);
+// polls of a wait of the paged attention before it gives up: a poll of a barrier that does not come takes up to about
+// 20 us, so a few seconds
+constexpr long long kPagedWaitLimit = 1 << 18;
 void paged_test_hooks(long long *wait_limit, int *idle_producer);
 
 }  // namespace sgd

@@ -67,6 +67,7 @@ struct Seq {
     int L, n, base;  // tokens, nodes, entries before the nodes
     int sink_tiles;  // tiles of the first tokens that do not belong to the window
     int first;       // the window's first tile
+    int win;         // the first entry of any window, 0 without one
     int tiles;       // >= 1
 };
 
@@ -84,9 +85,10 @@ __device__ __forceinline__ Seq seq_of(const PagedView &kv, const PagedAttnArgs &
     }
     s.base = s.L - s.n;
     const int all = (s.L + kTile - 1) / kTile;
-    s.sink_tiles = s.first = 0;
+    s.sink_tiles = s.first = s.win = 0;
     if (a.window) {
-        s.first = max(s.base + 1 - a.window, 0) / kTile;
+        s.win = max(s.base + 1 - a.window, 0);
+        s.first = s.win / kTile;
         s.sink_tiles = min((int)(((int64_t)a.sinks + kTile - 1) / kTile), s.first);
     }
     s.tiles = s.n == 0 ? 1 : max(1, s.sink_tiles + all - s.first);
@@ -100,7 +102,9 @@ struct Steps {
     int from, to;
     bool unseen;
 };
+__device__ __forceinline__ bool all_seen(const Seq &s, int t0) { return t0 + kTile <= s.L && t0 >= s.win; }
 __device__ __forceinline__ Steps steps_of(const Seq &s, const PagedAttnArgs &a, int t0) {
+    if (all_seen(s, t0)) return {0, kTile / 16, false};
     int lo = 0, hi = min(max(s.L - t0, 0), kTile);
     bool gap = false;
     if (a.window) {
@@ -438,11 +442,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (!go || !(go = wait_warp(&bar.p_full[g], np[g]++ & 1))) return false;
             tc_fence_after();
             const uint64_t dv = desc_mn_major(slot(pos), kTile * 128);
-            if (elect_one()) {
-#pragma unroll
-                for (int j = 0; j < kTile / 16; ++j)
-                    if (j >= st.from && j < st.to)
-                        mma_ts(tm + 256 + g * 128, tm + g * 128 + j * 8, dv + j * (2048 >> 4), ID_PV, acc || j > st.from);
+            if (elect_one()) {  // rolled: the unrolled loop, or two of them, cost the INT8 case 2 to 10% in instruction fetches
+#pragma unroll 1
+                for (int j = st.from; j < st.to; ++j)
+                    mma_ts(tm + 256 + g * 128, tm + g * 128 + j * 8, dv + j * (2048 >> 4), ID_PV, acc || j > st.from);
             }
             return true;
         };
@@ -468,7 +471,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (seg > 0 && !(go = wait_warp(&bar.o_free, (seg - 1) & 1))) break;  // the last segment's O was read
             for (int j = 0; j < T; ++j) {
                 const uint32_t v_at = at + pos_v<C::TWO>(j, T), k_at = at + pos_k<C::TWO>(C::TWO ? j + 1 : j + 2);
-                const Steps st = steps_of(w.s, a, tile_of(w.s, w.lo + j) * kTile);
+                const int t0 = tile_of(w.s, w.lo + j) * kTile;
+                Steps st = {0, kTile / 16, false};
+                if (__any_sync(0xffffffffu, !all_seen(w.s, t0))) {
+                    st = steps_of(w.s, a, t0);
+                    st.from = __shfl_sync(0xffffffffu, st.from, 0), st.to = __shfl_sync(0xffffffffu, st.to, 0);
+                }
                 if (!full(v_at)) break;
                 if (lane == 0 && st.unseen) {  // its rows may be cleared
                     mbar_arrive(&bar.v_here[C::TWO ? 0 : j & 1]);
@@ -700,21 +708,24 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         }
                         l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
                     }
-                    const Steps st = steps_of(s, a, t0);
-                    if (st.unseen) {  // clear V's rows once they are here
-                        if (!(go = wait_warp(&bar.v_here[g], nv++ & 1))) break;
-                        const uint32_t pos = at + pos_v<C::TWO>(j, T);
-                        uint8_t *v = smem + C::OFF_SLOT + (pos % C::SLOTS) * C::TILE_BYTES;
-                        auto zero = [&](int from, int to) {  // rows of the tile, 16 bytes a lane
-                            constexpr int PER = D / 8;
-                            from = max(from, st.from * 16), to = min(to, st.to * 16);
-                            for (int u = from * PER + wq * 32 + lane; u < to * PER; u += na * 32)
-                                *reinterpret_cast<uint4 *>(v + (u % PER) / 8 * kTile * 128 + u / PER * 128 + u % 8 * 16) =
-                                    make_uint4(0, 0, 0, 0);
-                        };
-                        zero(s.L - t0, kTile);
-                        if (a.window) zero(a.sinks - t0, v_lo - t0);
-                        fence_proxy_async_shared();
+                    if (!all_seen(s, t0)) {
+                        const Steps st = steps_of(s, a, t0);
+                        if (st.unseen) {  // clear V's rows once they are here
+                            if (!(go = wait_warp(&bar.v_here[g], nv++ & 1))) break;
+                            const uint32_t pos = at + pos_v<C::TWO>(j, T);
+                            uint8_t *v = smem + C::OFF_SLOT + (pos % C::SLOTS) * C::TILE_BYTES;
+                            auto zero = [&](int from, int to) {  // rows of the tile, 16 bytes a lane
+                                constexpr int PER = D / 8;
+                                from = max(from, st.from * 16), to = min(to, st.to * 16);
+#pragma unroll 1
+                                for (int u = from * PER + wq * 32 + lane; u < to * PER; u += na * 32)
+                                    *reinterpret_cast<uint4 *>(v + (u % PER) / 8 * kTile * 128 + u / PER * 128 + u % 8 * 16) =
+                                        make_uint4(0, 0, 0, 0);
+                            };
+                            zero(s.L - t0, kTile);
+                            if (a.window) zero(a.sinks - t0, v_lo - t0);
+                            fence_proxy_async_shared();
+                        }
                     }
                     tmem_wait_st();
                     tc_fence_before();
@@ -725,7 +736,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
                 if (!query) l = 0.f;
 
-                // the segment's result
+                // The segment's result.  A row that sees nothing has sum 0 exactly; a NaN (from its query) stays one.
                 const bool whole = w.lo == 0 && w.hi == s.tiles;
                 const int64_t out_row = (((int64_t)w.b * a.M + m) * kv.Hkv + w.h) * a.G + gh;
                 const int64_t part_row =
@@ -733,7 +744,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 float f0, f1 = 0.f, sum, ref;  // O_0 f0 + O_1 f1 is the normalised row
                 if constexpr (C::TWO) {
                     sum = l, ref = mx;
-                    f0 = sum > 0.f ? vs / sum : 0.f;
+                    f0 = sum != 0.f ? vs / sum : 0.f;
                 } else {
                     // every warp has read the last segment's pair
                     if (seg > 0 && !(go = wait_warp(&bar.o_free, (seg - 1) & 1))) break;
@@ -743,10 +754,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     if (!(go = wait_warp(&bar.ml_full, seg & 1))) break;
                     const float2 u = ml[r], v = ml[128 + r];
                     ref = fmaxf(u.x, v.x);
-                    const float e0 = u.y > 0.f ? ex2(u.x - ref) : 0.f, e1 = v.y > 0.f ? ex2(v.x - ref) : 0.f;
+                    const float e0 = u.y != 0.f ? ex2(u.x - ref) : 0.f, e1 = v.y != 0.f ? ex2(v.x - ref) : 0.f;
                     sum = e0 * u.y + e1 * v.y;
-                    f0 = sum > 0.f ? vs * e0 / sum : 0.f;
-                    f1 = sum > 0.f ? vs * e1 / sum : 0.f;
+                    f0 = sum != 0.f ? vs * e0 / sum : 0.f;
+                    f1 = sum != 0.f ? vs * e1 / sum : 0.f;
                 }
                 for (int i = 0; i < 2; ++i) {
                     if (C::TWO ? i != g : i >= T) continue;
@@ -788,7 +799,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.o_free);
                 if (valid && (C::TWO || g == 0)) {
-                    const float lse2 = sum > 0.f ? ref - C::SHIFT + log2f(sum) : -INFINITY;
+                    const float lse2 = sum != 0.f ? ref - C::SHIFT + log2f(sum) : -INFINITY;
                     if (whole) a.lse[out_row] = lse2 * 0.69314718055994531f;
                     else plan.lse_part[part_row] = lse2;
                 }
@@ -929,19 +940,19 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(PagedView kv
 #pragma unroll
         for (int i = 0; i < E; ++i) o[i] = 0.f;
         for (int w = 0; w < WARPS; ++w) {
-            const float f = sl[w] > 0.f ? ex2(sm[w] - mx) : 0.f;
+            const float f = sl[w] != 0.f ? ex2(sm[w] - mx) : 0.f;
             l += f * sl[w];
 #pragma unroll
             for (int i = 0; i < E; ++i) o[i] += f * so[w][lane * E + i];
         }
     }
-    const float f = l > 0.f ? 1.f / l : 0.f;
+    const float f = l != 0.f ? 1.f / l : 0.f;
     uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) + out_row * D) + lane * (E / 2);
     if constexpr (E == 4)
         *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(o[0] * f, o[1] * f), pack_bf16(o[2] * f, o[3] * f));
     else
         *dst = pack_bf16(o[0] * f, o[1] * f);
-    if (lane == 0) a.lse[out_row] = l > 0.f ? (mx + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    if (lane == 0) a.lse[out_row] = l != 0.f ? (mx + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 // ------------------------------------------------------------------------------------------ host

@@ -188,6 +188,23 @@ def test_attn_large_and_small_logits(sgd):
     check_attn(sgd, case, case.query(5, 8), 8)
 
 
+@pytest.mark.parametrize("dtype,M", [("bf16", 4), ("bf16", 40), ("int8", 4)])
+def test_attn_nan_query_stays_in_its_row(sgd, dtype, M):
+    case = Case((3000, 129), Hkv=1, dtype=dtype, seed=14)
+    q = case.query(M, 8)
+    clean = sgd.paged_attn(q.cuda(), 8, case.gpu(sgd))
+    q[0, 1, 3, 7] = float("nan")
+    q[1, 0, 0, :] = float("inf")
+    out, lse, _ = sgd.paged_attn(q.cuda(), 8, case.gpu(sgd))
+    bad = torch.zeros(lse.shape, dtype=torch.bool, device="cuda")
+    bad[0, 1, 3] = bad[1, 0, 0] = True
+    assert out[bad].isnan().all() and lse[bad].isnan().all()
+    # another row's reference may move at another tile (the warp's rows decide together): equal but for roundings
+    assert torch.isfinite(out[~bad]).all()
+    assert (out[~bad].float() - clean[0][~bad].float()).abs().max() <= 2.0 ** -7 * float(clean[0].float().abs().max())
+    assert (lse[~bad] - clean[1][~bad]).abs().max() <= 1e-4
+
+
 def test_attn_running_maximum_grows(sgd):
     # keys whose logits climb along the row, so that the running maximum moves in every tile
     L, D = 2000, 128
@@ -694,3 +711,26 @@ def test_selected_tokens_kept_in_pages(sgd):
     vmax = float(v.float().abs().max())
     assert (out[:, 0].float() - want).abs().max() <= 3 * 2.0 ** -8 * vmax
     assert (lse[:, 0] - want_lse).abs().max() <= 2e-3
+
+
+# ---------------------------------------------------------------------------------------------
+# waits that run out
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype,M", [("bf16", 1), ("bf16", 40), ("int8", 4), ("int8", 40)])
+def test_attn_waits_are_bounded(sgd, dtype, M):
+    # with the producer idle every wait on the pipeline runs out, nothing in flight: the call ends, says so, and the
+    # same call made afterwards is right
+    import time
+    case = Case((300, 2100, 70), dtype=dtype, seed=M)
+    q, par = case.query(M, 8), tree(case.rng, 3, M)
+    cache = case.gpu(sgd)
+    torch.cuda.synchronize()
+    sgd.test_pipeline_timeout(4096, True)
+    try:
+        t = time.perf_counter()
+        _, _, ws = sgd.paged_attn(q.cuda(), 8, cache, ints(par))
+        assert sgd.workspace_status(ws) & 0x2
+        assert time.perf_counter() - t < 20
+    finally:
+        sgd.test_pipeline_timeout(0, False)
+    check_attn(sgd, case, q, 8, parent=par, cache=cache)
