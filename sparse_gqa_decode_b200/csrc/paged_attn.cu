@@ -296,8 +296,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         prefetch_tensormap(&map_k);
         prefetch_tensormap(&map_v);
     }
-    if (tid == 32) bar.status = 0;
+    if (tid == 64) bar.status = 0;
     if (warp == kWarpMma) tmem_alloc(&bar.tmem, 512);
+    grid_dependency_wait();  // nothing of the call's data was touched so far
     __syncthreads();
 
     // the stream's length, this range of it, and the row it starts in: thread t sums consecutive rows
@@ -883,6 +884,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(PagedView kv
     constexpr int ROWS = kMergeThreads / 32 / WARPS;  // output rows of a CTA
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wr = warp % WARPS;
     const int Hq = kv.Hkv * a.G;
+    grid_dependency_wait();
     if (blockIdx.x == 0 && warp == 0) {  // the call's status
         int bits = 0;
         for (int c = lane; c < plan.n_cta; c += 32) bits |= plan.status[c];
@@ -1014,16 +1016,16 @@ int launch(const PagedView &kv, const PagedAttnArgs &a, const AttnPlan &plan, cu
     auto kern = paged_attn_kernel<C>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
         return SGD_ERR_CUDA;
-    const cudaError_t e = launch_k(kern, dim3(plan.n_ranges * plan.RT), dim3(C::THREADS), C::SMEM, s, 1, kv, a, plan,
-                                   mq, mk, mv);
+    const cudaError_t e =
+        launch_k_early(kern, dim3(plan.n_ranges * plan.RT), dim3(C::THREADS), C::SMEM, s, kv, a, plan, mq, mk, mv);
     if (e != cudaSuccess) return SGD_ERR_CUDA;
     // few rows may have many ranges each (up to all of them): then a CTA per row; many rows have few
     const int64_t n_rows = (int64_t)kv.B * a.M * kv.Hkv * a.G;
     constexpr int W = kMergeThreads / 32;
     if (n_rows <= 2048)
-        launch_k(paged_merge_kernel<C::D, W>, dim3((unsigned)n_rows), dim3(kMergeThreads), 0, s, 1, kv, a, plan, (int)C::TWO, n_rows);
+        launch_k_early(paged_merge_kernel<C::D, W>, dim3((unsigned)n_rows), dim3(kMergeThreads), 0, s, kv, a, plan, (int)C::TWO, n_rows);
     else
-        launch_k(paged_merge_kernel<C::D, 1>, dim3((unsigned)((n_rows + W - 1) / W)), dim3(kMergeThreads), 0, s, 1, kv, a, plan,
+        launch_k_early(paged_merge_kernel<C::D, 1>, dim3((unsigned)((n_rows + W - 1) / W)), dim3(kMergeThreads), 0, s, kv, a, plan,
                  (int)C::TWO, n_rows);
     return cudaGetLastError() == cudaSuccess ? SGD_OK : SGD_ERR_CUDA;
 }
