@@ -208,6 +208,12 @@ __device__ __forceinline__ float q_to_f16(uint8_t *q, int r) {
     return __uint_as_float((uint32_t)(127 - 13 + e) << 23);
 }
 
+// The polls after a wait's first one, out of line: two dozen copies of the loop would crowd the instruction cache.
+__device__ __noinline__ bool wait_on(uint64_t *m, uint32_t parity, int32_t *status, volatile int32_t *abort,
+                                     long long limit) {
+    return mbar_wait(m, parity, status, abort, limit);
+}
+
 // Walks a CTA's range: the same sequence of segments in every role.
 struct Walk {
     int b, h, start, x0, x1;  // item (b, h) starts at stream position `start`
@@ -334,7 +340,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // the first poll looks at nothing but the barrier: while the tensor cores read their operands a shared-memory
     // access takes a few hundred cycles, and the abort flag would double that
     auto wait = [&](uint64_t *m, uint32_t parity) {
-        return mbar_try_wait(m, parity) || mbar_wait(m, parity, &bar.status, abort, a.wait_limit);
+        return mbar_try_wait(m, parity) || wait_on(m, parity, &bar.status, abort, a.wait_limit);
     };
     // the same answer in every lane, so that the warp stays together
     auto wait_warp = [&](uint64_t *m, uint32_t parity) { return (bool)__all_sync(0xffffffffu, wait(m, parity)); };
