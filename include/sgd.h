@@ -422,8 +422,9 @@ typedef struct {
     int32_t *ref_count;       /* [n_pages]; may be NULL for sgd_paged_attn and sgd_pages_append */
 } sgd_paged_kv;
 
-/* Workspace bytes of every call that takes an sgd_paged_kv, with up to M query tokens and G query
- * heads per KV head.  Returns 0 on invalid arguments. */
+/* Workspace bytes for any of the calls that take an sgd_paged_kv: sgd_paged_attn with up to M query
+ * tokens and G query heads per KV head, and all upkeep calls; M = 0: the upkeep calls alone (of them
+ * only _reserve and _fork need more than 256 bytes).  Returns 0 on invalid arguments. */
 size_t sgd_paged_workspace_size(const sgd_paged_kv *kv, int G, int M);
 
 /*

@@ -586,7 +586,7 @@ def plan_segments(cu: torch.Tensor, B: int, Hkv: int, n_req: int, min_chunk: int
 # ------------------------------------------------------------------------------------------
 def _want(t, name: str, dtype, shape, device):
     """Raises ValueError unless ``t`` is a contiguous tensor of this dtype and shape on ``device``."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}" + ("" if t.is_contiguous() else ", strided"))
 
@@ -629,8 +629,9 @@ class PagedKv:
         return PagedKv(self.k, self.v, self.page_table, lens, self.held, self.ref_count, self.k_scale, self.v_scale)
 
 
-def paged_workspace_size(cache: PagedKv, G: int = 1, M: int = 1) -> int:
-    """Bytes of a workspace for any paged call with up to ``M`` query tokens and ``G`` heads per KV head."""
+def paged_workspace_size(cache: PagedKv, G: int = 1, M: int = 0) -> int:
+    """Bytes of a workspace for any paged call with up to ``M`` query tokens and ``G`` heads per KV head
+    (M = 0: for the upkeep calls alone)."""
     n = lib.sgd_paged_workspace_size(cache._ref, G, M)
     if n == 0:
         raise SgdError("sgd_paged_workspace_size rejected the arguments")
@@ -646,7 +647,7 @@ class _On:
         if device.type == "cuda" and device.index != torch.cuda.current_device():
             raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
         self.device, self.stream = device, stream
-        self.raw = (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+        self.raw = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
 
     def empty(self, shape, dtype):
         if self.stream is None:

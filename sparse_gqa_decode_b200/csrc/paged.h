@@ -1,9 +1,25 @@
 // paged.h -- host-side interface between the paged entry points (paged_api.cu) and their kernels.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace sgd {
+
+// A kernel's permission to use more shared memory than 48 KB, asked for once per device (the call costs a microsecond).
+struct SmemOptIn {
+    std::atomic<uint64_t> done{0};  // a bit per device; devices from 64 on ask every time
+    bool set(const void *kern, int bytes) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return false;
+        const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+        if (done.load(std::memory_order_relaxed) & bit) return true;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+        done.fetch_or(bit, std::memory_order_relaxed);
+        return true;
+    }
+};
 
 // An sgd_paged_kv as the kernels take it (device pointers).
 struct PagedView {

@@ -40,15 +40,17 @@ PagedView view(const sgd_paged_kv *kv) {
     return v;
 }
 
-// what the upkeep calls keep behind the header: a word per page and three per row
-size_t upkeep_bytes(const sgd_paged_kv *kv) { return ((size_t)kv->n_pages + 3 * (size_t)kv->B + 64) * 4; }
+// the upkeep calls: a word per page and three per row behind the header
+size_t upkeep_bytes(const sgd_paged_kv *kv) {
+    return sizeof(WsHeader) + (((size_t)kv->n_pages + 3 * (size_t)kv->B + 64) * 4 + 255) / 256 * 256;
+}
 
 // SMs of a B200; the partial results of the attention are sized for them whatever the device
 constexpr int kMaxSms = 148;
 
 size_t workspace_bytes_of(const sgd_paged_kv *kv, int G, int M) {
-    const size_t attn = paged_attn_scratch(kv->B, kv->Hkv, kv->D, G, M, kMaxSms);
-    return sizeof(WsHeader) + (std::max(upkeep_bytes(kv), attn) + 255) / 256 * 256;
+    if (M == 0) return upkeep_bytes(kv);
+    return std::max(upkeep_bytes(kv), sizeof(WsHeader) + paged_attn_scratch(kv->B, kv->Hkv, kv->D, G, M, kMaxSms));
 }
 
 // Checks the workspace and the device, and zeroes the status word unless the call's first kernel
@@ -75,7 +77,7 @@ using namespace sgd;
 extern "C" {
 
 size_t sgd_paged_workspace_size(const sgd_paged_kv *kv, int G, int M) {
-    if (check_paged(kv, false) != SGD_OK || G < 1 || G > 16 || M < 1 || M > SGD_MAX_NODES) return 0;
+    if (check_paged(kv, false) != SGD_OK || M < 0 || M > SGD_MAX_NODES || (M > 0 && (G < 1 || G > 16))) return 0;
     return workspace_bytes_of(kv, G, M);
 }
 
@@ -137,7 +139,7 @@ int sgd_pages_reserve(const sgd_paged_kv *kv, const int32_t *add, int32_t *new_l
     if (!aligned(add, 4) || !aligned(new_lens, 4)) return SGD_ERR_ALIGN;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int sms;
-    rc = begin(workspace, workspace_bytes, workspace_bytes_of(kv, 1, 1), false, s, &sms);
+    rc = begin(workspace, workspace_bytes, upkeep_bytes(kv), false, s, &sms);
     if (rc != SGD_OK) return rc;
     return launch_pages_reserve(view(kv), add, new_lens, scratch_of(workspace), status_of(workspace), s);
 }
@@ -165,7 +167,7 @@ int sgd_pages_fork(const sgd_paged_kv *kv, const int32_t *src, const int32_t *ds
     if (!aligned(src, 4) || !aligned(dst, 4)) return SGD_ERR_ALIGN;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int sms;
-    rc = begin(workspace, workspace_bytes, workspace_bytes_of(kv, 1, 1), false, s, &sms);
+    rc = begin(workspace, workspace_bytes, upkeep_bytes(kv), false, s, &sms);
     if (rc != SGD_OK) return rc;
     return launch_pages_fork(view(kv), src, dst, n, scratch_of(workspace), status_of(workspace), s);
 }

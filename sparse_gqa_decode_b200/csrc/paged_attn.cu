@@ -1020,8 +1020,8 @@ int launch(const PagedView &kv, const PagedAttnArgs &a, const AttnPlan &plan, cu
     if (!encode_fn() || !map_query(&mq, kv, a, plan.Mt) || !map_pool(&mk, kv.k, kv) || !map_pool(&mv, kv.v, kv))
         return SGD_ERR_CUDA;
     auto kern = paged_attn_kernel<C>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-        return SGD_ERR_CUDA;
+    static SmemOptIn opt_in;
+    if (!opt_in.set(reinterpret_cast<const void *>(kern), C::SMEM)) return SGD_ERR_CUDA;
     const cudaError_t e =
         launch_k_early(kern, dim3(plan.n_ranges * plan.RT), dim3(C::THREADS), C::SMEM, s, kv, a, plan, mq, mk, mv);
     if (e != cudaSuccess) return SGD_ERR_CUDA;

@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kAllocThreads) reserve_kernel(PagedView kv, co
                                                                 int32_t *status) {
     __shared__ int32_t sm[33];
     __shared__ unsigned long long wanted;
+    grid_dependency_wait();
     const int per = (kv.B + kAllocThreads - 1) / kAllocThreads;
     const int b0 = min((int)threadIdx.x * per, kv.B), b1 = min(b0 + per, kv.B);
     int bad = 0;
@@ -133,6 +134,7 @@ __global__ void __launch_bounds__(kAllocThreads) fork_plan_kernel(PagedView kv, 
                                                                   int32_t *mark, int32_t *fresh, int32_t *list,
                                                                   int32_t *go, int32_t *status) {
     __shared__ int32_t sm[33];
+    grid_dependency_wait();
     for (int b = threadIdx.x; b < kv.B; b += kAllocThreads) mark[b] = 0;
     __syncthreads();
     const int per = (n + kAllocThreads - 1) / kAllocThreads;
@@ -182,6 +184,7 @@ __global__ void __launch_bounds__(128) fork_copy_kernel(PagedView kv, const int3
                                                         const int32_t *__restrict__ dst,
                                                         const int32_t *__restrict__ fresh,
                                                         const int32_t *__restrict__ go, int32_t *status) {
+    grid_dependency_wait();
     if (*go == 0) return;
     const int i = blockIdx.x, h = blockIdx.y, s = src[i], d = dst[i];
     const int L = kv.lens[s], full = L / SGD_PAGE, to = fresh[i];
@@ -448,7 +451,8 @@ template <bool ACCEPT, int LANES>
 int launch_compact(const PagedView &kv, const CompactArgs &a, cudaStream_t s) {
     auto k = compact_kernel<ACCEPT, LANES>;
     constexpr int smem = sizeof(CompactShared<LANES>);
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return SGD_ERR_CUDA;
+    static SmemOptIn opt_in;
+    if (!opt_in.set(reinterpret_cast<const void *>(k), smem)) return SGD_ERR_CUDA;
     const dim3 grid(kv.B * kv.Hkv, 2, kv.D * kv.es / (LANES * 16));
     const cudaError_t e = launch_k(k, grid, dim3(kCompactThreads), smem, s, 1, kv, a);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? SGD_OK : SGD_ERR_CUDA;
@@ -460,15 +464,15 @@ bool ok() { return cudaGetLastError() == cudaSuccess; }
 
 int launch_pages_reserve(const PagedView &kv, const int32_t *add, int32_t *new_lens, int32_t *scratch,
                          int32_t *status, cudaStream_t s) {
-    launch_k(reserve_kernel, dim3(1), dim3(kAllocThreads), 0, s, 1, kv, add, new_lens, scratch, scratch + kv.B, status);
+    launch_k_early(reserve_kernel, dim3(1), dim3(kAllocThreads), 0, s, kv, add, new_lens, scratch, scratch + kv.B, status);
     return ok() ? SGD_OK : SGD_ERR_CUDA;
 }
 
 int launch_pages_fork(const PagedView &kv, const int32_t *src, const int32_t *dst, int n, int32_t *scratch,
                       int32_t *status, cudaStream_t s) {
     int32_t *mark = scratch, *fresh = mark + kv.B, *go = fresh + kv.B, *list = go + 1;
-    launch_k(fork_plan_kernel, dim3(1), dim3(kAllocThreads), 0, s, 1, kv, src, dst, n, mark, fresh, list, go, status);
-    launch_k(fork_copy_kernel, dim3(n, kv.Hkv, 2), dim3(128), 0, s, 1, kv, src, dst, fresh, go, status);
+    launch_k_early(fork_plan_kernel, dim3(1), dim3(kAllocThreads), 0, s, kv, src, dst, n, mark, fresh, list, go, status);
+    launch_k_early(fork_copy_kernel, dim3(n, kv.Hkv, 2), dim3(128), 0, s, kv, src, dst, fresh, go, status);
     return ok() ? SGD_OK : SGD_ERR_CUDA;
 }
 
