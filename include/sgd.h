@@ -400,7 +400,9 @@ int sgd_decode_attn_noalloc(const void *q, sgd_dtype q_dtype, int G, const sgd_k
  * Sequence b (a row of the page table) holds lens[b] tokens; its token t is slot t % 64 of page
  * page_table[b * max_pages + t / 64].  A page belongs to every row that lists it among its first
  * held[b] entries; ref_count[p] counts them, and 0 means free.  Slots behind the last token
- * may hold anything, NaN included, and are left as they are.
+ * may hold anything, NaN included, and are left as they are.  A workspace serves one call at a
+ * time: calls that may overlap on the GPU (two streams, two graphs) take one each.  Outputs
+ * overlap no input unless a call's comment says so.
  * ------------------------------------------------------------------------------------------ */
 #define SGD_PAGE 64       /* tokens of a page */
 #define SGD_MAX_NODES 64  /* query tokens of a sequence in one step of the paged calls */
@@ -444,7 +446,8 @@ size_t sgd_paged_workspace_size(const sgd_paged_kv *kv, int G, int M);
  * window   >= 0, 0 = unlimited; sinks >= 0, read with a window only
  * out      [B, M, Hq, D] BF16; lse [B, M, Hq] float32, natural log
  * K and V of an entry that no query of the sequence sees may be anything; those of an entry that
- * some query sees must be finite.
+ * some query sees must be finite.  A query with a NaN gets NaN, alone.  B * Hkv * (max_pages / 2 + 4)
+ * stays below 2^31 (SGD_ERR_SHAPE).
  * Status: BAD_INDEX for a page outside the pool (page 0 is read), a parent outside [-1, m) (taken
  * as -1) or n_nodes outside [0, M] (clamped); SIZE_MISMATCH for lens[b] outside
  * [0, 64 * max_pages] (clamped); BAD_SCALE as in sgd_quantize_kv.

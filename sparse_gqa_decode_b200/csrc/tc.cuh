@@ -151,42 +151,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// two floats in a register pair, and packed arithmetic on them
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-    return (uint64_t)__float_as_uint(lo) | (uint64_t)__float_as_uint(hi) << 32;
-}
-__device__ __forceinline__ float lo_of(uint64_t x) { return __uint_as_float((uint32_t)x); }
-__device__ __forceinline__ float hi_of(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-// 2^x of two floats on the multiply-add units, for x <= 127 (below -126 as -126): x = n + r with n the
-// nearest integer, |r| <= 1/2, 2^r by the degree-5 polynomial of least relative error there (1.5e-7
-// with these float32 coefficients, found by Lawson's reweighted least squares), n into the exponent.
-__device__ __forceinline__ uint64_t ex2_poly2(uint64_t x) {
-    const float magic = 12582912.f;  // 1.5 * 2^23: adding it leaves n in the low mantissa bits
-    x = pair(fmaxf(lo_of(x), -126.f), fmaxf(hi_of(x), -126.f));
-    const uint64_t t = add2(x, pair(magic, magic));
-    const uint64_t r = fma2(add2(t, pair(-magic, -magic)), pair(-1.f, -1.f), x);
-    uint64_t p = pair(1.3276472454890609e-03f, 1.3276472454890609e-03f);
-    p = fma2(p, r, pair(9.675541892647743e-03f, 9.675541892647743e-03f));
-    p = fma2(p, r, pair(5.550713092088699e-02f, 5.550713092088699e-02f));
-    p = fma2(p, r, pair(2.4022120237350464e-01f, 2.4022120237350464e-01f));
-    p = fma2(p, r, pair(6.931469440460205e-01f, 6.931469440460205e-01f));
-    p = fma2(p, r, pair(1.0000001192092896f, 1.0000001192092896f));
-    const uint32_t lo = (uint32_t)p + ((uint32_t)t << 23);
-    const uint32_t hi = (uint32_t)(p >> 32) + ((uint32_t)(t >> 32) << 23);
-    return (uint64_t)lo | (uint64_t)hi << 32;
-}
-
 // 4-D tiled TMA load of one box into shared memory, completing on `bar` (tx bytes).
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z,
                                             int w) {

@@ -687,6 +687,75 @@ def test_speculative_steps(sgd, dtype):
             same_state(cache, st)
 
 
+def test_captured_step_replays(sgd):
+    """A whole speculative step in one graph, replayed on changing inputs, against the same calls made one by one."""
+    rng = np.random.default_rng(5)
+    B, M, Hkv, G, D, V = 3, 6, 2, 8, 64, 9001
+    case = Case((70, 640, 1), Hkv=Hkv, D=D, seed=6, spare=20, max_pages=14)
+    n = ints([6, 4, 5])
+    cu = ints([0, 6, 10, 15])
+    shapes = dict(k=(Hkv, 15, D), v=(Hkv, 15, D), q=(B, M, Hkv * G, D))
+    x = {a: torch.zeros(sh, dtype=torch.bfloat16, device="cuda") for a, sh in shapes.items()}
+    x |= dict(p=torch.zeros(B, M, V, device="cuda"), dr=torch.zeros(B, M, V, device="cuda"), tok=ints(np.zeros((B, M))),
+              par=ints(tree(rng, B, M)), ua=torch.zeros(B, M, device="cuda"), us=torch.zeros(B, device="cuda"))
+
+    def step(cache):
+        grown, w0 = sgd.pages_reserve(cache, n)
+        c = cache.with_lens(grown)
+        w1 = sgd.pages_append(c, x["k"], x["v"], cu)
+        out, lse, w2 = sgd.paged_attn(x["q"], G, c, x["par"], n, window=300, sinks=3)
+        n_path, path, token, w3 = sgd.verify_tree(x["p"], x["tok"], x["par"], x["ua"], x["us"], q=x["dr"], n_nodes=n)
+        new, w4 = sgd.pages_accept(c, path, n_path, n)
+        w5 = sgd.pages_release(c, new)
+        cache.lens.copy_(new)
+        return out, lse, n_path, path, token, [w0, w1, w2, w3, w4, w5]
+
+    eager, replayed = case.gpu(sgd), case.gpu(sgd)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):  # the kernels are loaded before the capture
+        step(case.gpu(sgd))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step(replayed)
+    for turn in range(4):
+        for a in ("k", "v", "q"):
+            x[a].copy_(torch.from_numpy(rng.standard_normal(shapes[a], dtype=np.float32)))
+        p, dr = _distributions(rng, B, M, V, "f32")
+        par = tree(rng, B, M)
+        tok = np.array([[int(np.argmax(dr[b, max(par[b, m], 0)].numpy() * rng.random(V))) for m in range(M)] for b in range(B)])
+        for a, t in (("p", p), ("dr", dr), ("tok", ints(tok)), ("par", ints(par)), ("ua", torch.from_numpy(rng.random((B, M)))),
+                     ("us", torch.from_numpy(rng.random(B)))):
+            x[a].copy_(t)
+        want = step(eager)
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got[:5], want[:5]):
+            assert torch.equal(a, b)
+        assert all(sgd.workspace_status(w) == 0 for w in got[5] + want[5])
+        for name in ("k", "v", "page_table", "lens", "held", "ref_count"):
+            a, b = getattr(eager, name), getattr(replayed, name)
+            assert torch.equal(a.nan_to_num(7.0) if name in "kv" else a, b.nan_to_num(7.0) if name in "kv" else b), name
+
+
+def test_calls_on_two_streams_at_once(sgd):
+    # two batches in flight at the same time, each with its own workspace, several times over
+    cases = [Case([int(x) for x in np.random.default_rng(s).integers(100, 5000, 12)], Hkv=4, seed=s) for s in (1, 2)]
+    qs = [c.query(5, 8).cuda() for c in cases]
+    caches = [c.gpu(sgd) for c in cases]
+    want = [sgd.paged_attn(q, 8, c) for q, c in zip(qs, caches)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(10):
+        for i in (0, 1):
+            got[i].append(sgd.paged_attn(qs[i], 8, caches[i], stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for out, lse, ws in got[i]:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1]) and sgd.workspace_status(ws) == 0
+
+
 def test_selected_tokens_kept_in_pages(sgd):
     """oam_select's kept set, made permanent in the pages: the paged attention over what is left is the
     kept-set decode over the packed cache."""
