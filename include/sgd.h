@@ -491,8 +491,9 @@ int sgd_verify_tree(const void *p, sgd_dtype p_dtype, const void *q, int B, int 
  * itself stays: pass new_lens as the next calls' lens).
  * The call changes nothing (new_lens = lens) and sets NO_PAGES where the free pages do not
  * suffice, SIZE_MISMATCH where a row would pass max_pages or add, lens or held is out of range,
- * SHARED_PAGE where a row would grow inside a page that another row holds too, BAD_INDEX where
- * the page it would grow in is outside the pool.
+ * SHARED_PAGE where a row would grow inside a page that another row holds too (a row cut back in
+ * pages that it shares gives those behind its end back first: sgd_pages_release), BAD_INDEX where
+ * a held page that it would grow in is outside the pool.
  * add      [B] int32, >= 0;  new_lens [B] int32 (may be lens itself)
  */
 int sgd_pages_reserve(const sgd_paged_kv *kv, const int32_t *add, int32_t *new_lens, void *workspace,
@@ -501,7 +502,8 @@ int sgd_pages_reserve(const sgd_paged_kv *kv, const int32_t *add, int32_t *new_l
 /*
  * sgd_pages_append -- K and V of new tokens into the pages: of row b the tokens
  * cu_new[b] .. cu_new[b+1] - 1 of k_new and v_new become its last cu_new[b+1] - cu_new[b] entries
- * (lens[b] counts them already, as after sgd_pages_reserve).  An I8 cache takes their codes under
+ * (lens[b] counts them already, as after sgd_pages_reserve, which refuses pages that another row
+ * holds too; a row is not forked between the two calls).  An I8 cache takes their codes under
  * its scales, as sgd_quantize_kv with SGD_SCHEME_B_CALIBRATED makes them.
  * k_new, v_new   [Hkv, T_new, D] BF16;  cu_new [B+1] int32, T_new = cu_new[B] (host value)
  * Status: BAD_INDEX for a page outside the pool, SIZE_MISMATCH for a token outside the row or a

@@ -152,8 +152,10 @@ class Pages:
             if (self.lens[b] < 0 or add[b] < 0 or not 0 <= self.held[b] <= self.table.shape[1] or
                     self.lens[b] > self.held[b] * PAGE or self.lens[b] + add[b] > self.table.shape[1] * PAGE):
                 status |= SIZE_MISMATCH
-            elif self.lens[b] % PAGE and add[b] and self.ref[self.table[b, self.lens[b] // PAGE]] > 1:
-                status |= SHARED_PAGE
+            elif add[b]:  # the held pages that it would grow in
+                last = min(int(self.held[b]), -(-(int(self.lens[b]) + int(add[b])) // PAGE))
+                if (self.ref[self.table[b, self.lens[b] // PAGE:last]] > 1).any():
+                    status |= SHARED_PAGE
         if status:
             return self.lens.copy(), status
         need = [max(0, -(-(int(L) + int(a)) // PAGE) - int(h)) for L, a, h in zip(self.lens, add, self.held)]

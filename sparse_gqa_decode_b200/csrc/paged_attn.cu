@@ -140,8 +140,7 @@ struct Cfg {
     static constexpr bool I8 = I8_, TWO = TWO_;
     static constexpr int HALVES = D / 64;                 // 64-channel halves, 16 KB each of a tile
     static constexpr int TILE_BYTES = kTile * D * 2;
-    // Q: the two row tiles, or two segments'; one segment's with codes, whose tiles in flight need the space (64 KB
-    // of codes in flight, released only once widened, hold a third of HBM's rate back)
+    // Q: the two row tiles, or two segments'; one segment's with codes, whose tiles in flight need the space
     static constexpr int Q_STAGES = TWO || I8 ? 1 : 2, Q_BUFS = TWO ? 2 : Q_STAGES;
     static constexpr int SLOTS = I8 ? (D == 128 ? 3 : 4) : (D == 128 ? 5 : 8);  // 16-bit tiles of K or V
     static constexpr int RAW = !I8 ? 0 : D == 128 ? (TWO ? 4 : 6) : (TWO ? 8 : 12);  // code tiles in flight

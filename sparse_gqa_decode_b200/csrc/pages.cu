@@ -88,8 +88,9 @@ __global__ void __launch_bounds__(kAllocThreads) reserve_kernel(PagedView kv, co
             bad |= SGD_STATUS_SIZE_MISMATCH;
             continue;
         }
-        if (L % SGD_PAGE != 0 && a > 0) {
-            const int p = kv.table[(int64_t)b * kv.max_pages + L / SGD_PAGE];
+        // the held pages that it grows in: the part-filled last one, and any behind the last token
+        for (int j = L / SGD_PAGE; a > 0 && j < min(h, ceil_pages(L + a)); ++j) {
+            const int p = kv.table[(int64_t)b * kv.max_pages + j];
             if (p < 0 || p >= kv.n_pages) bad |= SGD_STATUS_BAD_INDEX;
             else if (kv.ref[p] > 1) bad |= SGD_STATUS_SHARED_PAGE;
         }

@@ -458,6 +458,36 @@ def test_reserve_refuses_whole_calls(sgd):
     assert cache.lens.tolist() == [100, 64, 15, 0]
 
 
+def test_reserve_refuses_shared_pages_behind_the_last_token(sgd):
+    """A forked row that was cut back at a page's end would grow inside the pages that it still shares."""
+    for cut, add in ((64, 1), (64, 65), (0, 1), (0, 200), (10, 1), (128, 70)):
+        case = Case((192,), seed=cut, spare=6, rows=1, max_pages=6)
+        cache, st = case.gpu(sgd), case.host()
+        sgd.pages_fork(cache, ints([0]), ints([1]))
+        assert st.fork(np.array([0]), np.array([1])) == 0
+        cache.lens[0] = cut
+        st.lens[0] = cut
+        want, status = st.reserve(np.array([add, 0]))
+        assert status == 0x40
+        new, ws = sgd.pages_reserve(cache, ints([add, 0]))
+        assert sgd.workspace_status(ws) == 0x40 and new.tolist() == want.tolist()
+        same_state(cache, st)
+        # given back first, the row grows in pages of its own (unless it was cut inside one)
+        sgd.pages_release(cache, cache.lens)
+        st.release(st.lens)
+        want, status = st.reserve(np.array([add, 0]))
+        assert status == (0x40 if cut % PAGE else 0)
+        new, ws = sgd.pages_reserve(cache, ints([add, 0]))
+        assert sgd.workspace_status(ws) == status and new.tolist() == want.tolist()
+        same_state(cache, st)
+    case = Case((64, 10), seed=3, spare=2, max_pages=4, hold=(128, 64))
+    cache = case.gpu(sgd)
+    cache.page_table[0, 1] = case.n_pages
+    for add, status in ((0, 0), (1, 0x8)):
+        new, ws = sgd.pages_reserve(cache, ints([add, 1]))
+        assert sgd.workspace_status(ws) == status and new.tolist() == ([64, 10] if status else [64, 11])
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("Hkv", [1, 3])
 def test_append(sgd, D, Hkv):
