@@ -516,7 +516,7 @@ int sgd_pages_append(const sgd_paged_kv *kv, const void *k_new, const void *v_ne
  * sgd_pages_fork -- row dst[i] becomes a copy of row src[i], i < n: full pages are shared
  * (ref_count + 1), the tokens of a part-filled last page are copied into a free page, lowest page
  * first in the order of i; page table, lens, held and ref_count of the new rows follow.
- * src, dst [n] int32 row numbers; every dst once, none of them a src, with held[dst] = 0
+ * src, dst [n] int32 row numbers, n >= 1; every dst once, none of them a src, with held[dst] = 0
  * The call changes nothing and sets NO_PAGES where the free pages do not suffice, BAD_INDEX for
  * rows against those rules or a part-filled page outside the pool, SIZE_MISMATCH for a src whose
  * lens, held and max_pages disagree.  A full page outside the pool sets BAD_INDEX and is entered
@@ -552,7 +552,8 @@ int sgd_pages_accept(const sgd_paged_kv *kv, const int32_t *path, const int32_t 
  * sgd_pages_keep -- token dropping made permanent: of row b and KV head h the tokens
  * idx[h, cu_kept[b] .. cu_kept[b+1] - 1] (ascending, as sgd_oam_select writes them) become its
  * first ones, in order; new_lens[b] = cu_kept[b+1] - cu_kept[b].  A row with none keeps none.
- * idx      [Hkv, kept_total] int32; cu_kept [B+1] int32; new_lens [B] int32, not lens itself
+ * idx      [Hkv, kept_total] int32, kept_total >= 1; cu_kept [B+1] int32; new_lens [B] int32, not
+ *          lens itself
  * Status as in sgd_pages_accept.  The pages that fell empty are given back by
  * sgd_pages_release(kv, new_lens, ...).
  */

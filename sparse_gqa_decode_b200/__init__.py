@@ -692,7 +692,8 @@ def paged_attn(q: torch.Tensor, G: int, cache: PagedKv, parent=None, n_nodes=Non
         _want(lse, "lse", torch.float32, (cache.B, M, Hq), dev)
     ws = on.workspace(0 if workspace is not None else paged_workspace_size(cache, G, M), workspace)
     _check(lib.sgd_paged_attn(q.data_ptr(), G, M, cache._ref, None if parent is None else parent.data_ptr(),
-                              None if n_nodes is None else n_nodes.data_ptr(), window, sinks, o.data_ptr(),
+                              None if n_nodes is None else n_nodes.data_ptr(), min(window, 2 ** 31 - 1),
+                              min(sinks, 2 ** 31 - 1), o.data_ptr(),
                               lse.data_ptr(), ws.data_ptr(), _nbytes(ws), on.raw), "sgd_paged_attn")
     return o, lse, ws
 

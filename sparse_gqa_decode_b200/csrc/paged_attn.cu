@@ -318,9 +318,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (bad && blockIdx.x == 0) atomicOr(&bar.status, bad);
         int total;
         int pos = block_exclusive_scan(sum, total, reinterpret_cast<int32_t *>(smem + C::OFF_ML));
-        const int S = (total + plan.n_ranges - 1) / plan.n_ranges;
-        x0 = min((int64_t)range * S, (int64_t)total);
-        x1 = min(x0 + S, total);
+        const int S = total / plan.n_ranges + (total % plan.n_ranges != 0);  // total may be close to 2^31
+        x0 = (int)min((int64_t)range * S, (int64_t)total);
+        x1 = (int)min((int64_t)x0 + S, (int64_t)total);
         if (x0 < x1 && pos <= x0 && x0 < pos + sum) {
             for (int b = b0; b < b1; ++b) {
                 const int len = (seq_of(kv, a, b, bad).tiles + kItemCharge) * kv.Hkv;
@@ -724,7 +724,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             uint8_t *v = smem + C::OFF_SLOT + (pos % C::SLOTS) * C::TILE_BYTES;
                             auto zero = [&](int from, int to) {  // rows of the tile, 16 bytes a lane
                                 constexpr int PER = D / 8;
-                                from = max(from, st.from * 16), to = min(to, st.to * 16);
+                                // both ends first: a window or a row may lie 2^30 entries away
+                                from = min(max(from, st.from * 16), st.to * 16), to = min(max(to, 0), st.to * 16);
 #pragma unroll 1
                                 for (int u = from * PER + wq * 32 + lane; u < to * PER; u += na * 32)
                                     *reinterpret_cast<uint4 *>(v + (u % PER) / 8 * kTile * 128 + u / PER * 128 + u % 8 * 16) =

@@ -151,6 +151,20 @@ def test_attn_window(sgd, dtype, window, sinks, M):
     check_attn(sgd, case, case.query(M, 4), 4, parent=tree(case.rng, 5, M), window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "int8"])
+@pytest.mark.parametrize("M", [3, 40])
+def test_attn_windows_and_sinks_of_any_size(sgd, dtype, M):
+    """More than any position, up to sizes past 32 bits: all tokens are in the window, or among the first ones."""
+    case = Case((300, 70), seed=5, dtype=dtype)
+    q = torch.randn(2, M, 8, 128, device="cuda").bfloat16()
+    cache = case.gpu(sgd)
+    want = sgd.paged_attn(q, 4, cache)
+    big = [1000, 2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 40] + [x + d for n in range(20, 31) for x in (2 ** n, 3 * 2 ** (n - 1)) for d in (-1, 1)]
+    for kw in [dict(window=x) for x in big] + [dict(window=1, sinks=x) for x in big] + [dict(window=x, sinks=x) for x in big]:
+        got = sgd.paged_attn(q, 4, cache, **kw)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), kw
+
+
 def test_attn_window_over_evicted_tokens(sgd):
     # entries that no query of the row sees may hold anything: NaN in K and V between the first
     # tokens and the window, up to the edge of either
