@@ -554,8 +554,10 @@ int sgd_pages_accept(const sgd_paged_kv *kv, const int32_t *path, const int32_t 
  * first ones, in order; new_lens[b] = cu_kept[b+1] - cu_kept[b].  A row with none keeps none.
  * idx      [Hkv, kept_total] int32, kept_total >= 1; cu_kept [B+1] int32; new_lens [B] int32, not
  *          lens itself
- * Status as in sgd_pages_accept.  The pages that fell empty are given back by
- * sgd_pages_release(kv, new_lens, ...).
+ * Status: BAD_INDEX and SHARED_PAGE as in sgd_pages_accept (a list that does not ascend or leaves the
+ * row), SIZE_MISMATCH for a row whose range of cu_kept descends, leaves [0, kept_total] or is longer than
+ * the row, or whose lens is out of range (left as it is, new_lens = lens).  The pages that fell empty
+ * are given back by sgd_pages_release(kv, new_lens, ...).
  */
 int sgd_pages_keep(const sgd_paged_kv *kv, const int32_t *idx, const int32_t *cu_kept, int64_t kept_total,
                    int32_t *new_lens, void *workspace, size_t workspace_bytes, void *stream);

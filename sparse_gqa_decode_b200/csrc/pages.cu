@@ -336,6 +336,11 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(PagedView k
     const int b = blockIdx.x / kv.Hkv, h = blockIdx.x % kv.Hkv;
     int L = kv.lens[b], bad = 0, n, base = 0, limit;
     const int32_t *list;
+    auto leave = [&](int why) {  // the row stays as it is, and a release that follows takes nothing from it
+        if (threadIdx.x != 0) return;
+        atomicOr(a.status, why);
+        if (h == 0 && blockIdx.y == 0 && blockIdx.z == 0) a.new_lens[b] = L;
+    };
     if (L < 0 || L > (int64_t)kv.max_pages * SGD_PAGE) bad = SGD_STATUS_SIZE_MISMATCH;
     const int len = min(max(L, 0), kv.max_pages * SGD_PAGE);
     if constexpr (ACCEPT) {
@@ -347,12 +352,10 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(PagedView k
         list = a.path + (int64_t)b * a.M;
     } else {
         const int64_t c0 = a.cu_kept[b], c1 = a.cu_kept[b + 1];
-        n = 0;
-        if (c0 < 0 || c1 < c0 || c1 > a.kept_total || c1 - c0 > len) bad |= SGD_STATUS_SIZE_MISMATCH;
-        else n = (int)(c1 - c0);
-        if (bad) n = 0;
+        if (bad || c0 < 0 || c1 < c0 || c1 > a.kept_total || c1 - c0 > len) return leave(SGD_STATUS_SIZE_MISMATCH);
+        n = (int)(c1 - c0);
         limit = len;
-        list = a.idx + (int64_t)h * a.kept_total + (bad ? 0 : c0);
+        list = a.idx + (int64_t)h * a.kept_total + c0;
     }
     const int32_t *row = kv.table + (int64_t)b * kv.max_pages;
     // the pages written to: base / 64 .. (base + n - 1) / 64
@@ -362,13 +365,7 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(PagedView k
         if (p < 0 || p >= kv.n_pages) bad |= SGD_STATUS_BAD_INDEX;
         else if (kv.ref[p] > 1) shared = 1;
     }
-    if (__syncthreads_or(shared)) {
-        if (threadIdx.x == 0) {
-            atomicOr(a.status, SGD_STATUS_SHARED_PAGE);
-            if (h == 0 && blockIdx.y == 0 && blockIdx.z == 0) a.new_lens[b] = L;
-        }
-        return;
-    }
+    if (__syncthreads_or(shared)) return leave(SGD_STATUS_SHARED_PAGE);
     if (threadIdx.x == 0 && h == 0 && blockIdx.y == 0 && blockIdx.z == 0) a.new_lens[b] = base + n;
 
     extern __shared__ __align__(16) uint8_t smem[];
