@@ -420,7 +420,8 @@ typedef struct {
     const float *v_scale;     /* I8: [1] */
     int32_t *page_table;      /* [B, max_pages] */
     int32_t *lens;            /* [B] */
-    int32_t *held;            /* [B]; read by _reserve, _fork and _release (may be NULL for the others) */
+    int32_t *held;            /* [B]; needed by _reserve, _fork and _release; _accept and _keep check a row against it
+                               * where it is not NULL */
     int32_t *ref_count;       /* [n_pages]; may be NULL for sgd_paged_attn and sgd_pages_append */
 } sgd_paged_kv;
 
@@ -528,7 +529,9 @@ int sgd_pages_fork(const sgd_paged_kv *kv, const int32_t *src, const int32_t *ds
 /*
  * sgd_pages_release -- every row b gives back the pages behind its first keep[b] tokens: entries
  * ceil(keep[b] / 64) .. held[b] - 1 of its page table lose a reference, held[b] shrinks.  keep 0
- * ends a row, keep = lens[b] returns what was reserved and not used.  lens is not touched.
+ * ends a row, keep = lens[b] returns what was reserved and not used.  lens is not touched: the
+ * caller sets it to the kept length, 0 for an ended row.  The upkeep calls refuse a row that is longer than
+ * its held pages, sgd_pages_reserve all rows of the call with it.
  * keep     [B] int32, >= 0
  * Status: BAD_INDEX for a page outside the pool or without references (skipped), SIZE_MISMATCH
  * for a negative keep (taken as 0) or held[b] outside [0, max_pages] (clamped).
@@ -543,7 +546,9 @@ int sgd_pages_release(const sgd_paged_kv *kv, const int32_t *keep, void *workspa
  * path     [B, M] int32; n_path, n_nodes [B] int32; new_lens [B] int32, not lens itself
  * Status: BAD_INDEX for a path that does not ascend or leaves the nodes (clamped) or a page outside
  * the pool, SIZE_MISMATCH for counts out of range (clamped), SHARED_PAGE for a row that would
- * write a shared page (left as it is, new_lens = lens).
+ * write a shared page (left as it is, new_lens = lens).  A row that would write a page without
+ * references (BAD_INDEX) or is longer than its held pages (SIZE_MISMATCH; not checked where held is
+ * NULL) is left as it is, too.
  */
 int sgd_pages_accept(const sgd_paged_kv *kv, const int32_t *path, const int32_t *n_path, const int32_t *n_nodes,
                      int M, int32_t *new_lens, void *workspace, size_t workspace_bytes, void *stream);
@@ -556,8 +561,8 @@ int sgd_pages_accept(const sgd_paged_kv *kv, const int32_t *path, const int32_t 
  *          lens itself
  * Status: BAD_INDEX and SHARED_PAGE as in sgd_pages_accept (a list that does not ascend or leaves the
  * row), SIZE_MISMATCH for a row whose range of cu_kept descends, leaves [0, kept_total] or is longer than
- * the row, or whose lens is out of range (left as it is, new_lens = lens).  The pages that fell empty
- * are given back by sgd_pages_release(kv, new_lens, ...).
+ * the row, or whose lens is out of range or more than its held pages (left as it is, new_lens = lens).
+ * The pages that fell empty are given back by sgd_pages_release(kv, new_lens, ...).
  */
 int sgd_pages_keep(const sgd_paged_kv *kv, const int32_t *idx, const int32_t *cu_kept, int64_t kept_total,
                    int32_t *new_lens, void *workspace, size_t workspace_bytes, void *stream);

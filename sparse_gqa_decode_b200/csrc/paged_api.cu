@@ -193,7 +193,7 @@ int sgd_pages_accept(const sgd_paged_kv *kv, const int32_t *path, const int32_t 
     if (M < 1 || M > SGD_MAX_NODES) return SGD_ERR_SHAPE;
     if (new_lens == kv->lens) return SGD_ERR_ARG;
     if (!aligned(path, 4) || !aligned(n_path, 4) || !aligned(n_nodes, 4) || !aligned(new_lens, 4) ||
-        !aligned(kv->ref_count, 4))
+        !aligned(kv->ref_count, 4) || !aligned(kv->held, 4))
         return SGD_ERR_ALIGN;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int sms;
@@ -212,7 +212,8 @@ int sgd_pages_keep(const sgd_paged_kv *kv, const int32_t *idx, const int32_t *cu
     if (!idx || !cu_kept || !new_lens || !kv->ref_count) return SGD_ERR_NULL;
     if (kept_total < 1 || kept_total >= (int64_t(1) << 31)) return SGD_ERR_SHAPE;
     if (new_lens == kv->lens) return SGD_ERR_ARG;
-    if (!aligned(idx, 4) || !aligned(cu_kept, 4) || !aligned(new_lens, 4) || !aligned(kv->ref_count, 4))
+    if (!aligned(idx, 4) || !aligned(cu_kept, 4) || !aligned(new_lens, 4) || !aligned(kv->ref_count, 4) ||
+        !aligned(kv->held, 4))
         return SGD_ERR_ALIGN;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int sms;

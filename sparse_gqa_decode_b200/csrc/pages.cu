@@ -358,14 +358,18 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(PagedView k
         list = a.idx + (int64_t)h * a.kept_total + c0;
     }
     const int32_t *row = kv.table + (int64_t)b * kv.max_pages;
+    // a row that was released but still has its old length lists pages that are free, or another row's by now
+    if (kv.held && len > (int64_t)kv.held[b] * SGD_PAGE) return leave(SGD_STATUS_SIZE_MISMATCH);
     // the pages written to: base / 64 .. (base + n - 1) / 64
-    int shared = 0;
+    int shared = 0, vacant = 0;
     for (int j = base / SGD_PAGE + threadIdx.x; j < ceil_pages(base + n) && n > 0; j += kCompactThreads) {
         const int p = row[j];
         if (p < 0 || p >= kv.n_pages) bad |= SGD_STATUS_BAD_INDEX;
         else if (kv.ref[p] > 1) shared = 1;
+        else if (kv.ref[p] < 1) vacant = 1;
     }
     if (__syncthreads_or(shared)) return leave(SGD_STATUS_SHARED_PAGE);
+    if (__syncthreads_or(vacant)) return leave(SGD_STATUS_BAD_INDEX);
     if (threadIdx.x == 0 && h == 0 && blockIdx.y == 0 && blockIdx.z == 0) a.new_lens[b] = base + n;
 
     extern __shared__ __align__(16) uint8_t smem[];

@@ -38,3 +38,37 @@ def test_keep_leaves_rows_with_wrong_counts(sgd, cu, wrong):
     held = [-(-int(n) // PAGE) for n in want]
     held[wrong] = int(case.held[wrong])
     assert cache.held.tolist() == held and int(cache.ref_count.sum()) == sum(held)
+
+
+@pytest.mark.parametrize("call", ["keep", "accept"])
+@pytest.mark.parametrize("taken", [True, False])
+def test_compaction_of_an_ended_row_writes_nothing(sgd, call, taken):
+    """A row that was released but still has its old length: its table lists pages that are free, or another row's."""
+    case = Case((200, 64, 130), seed=11, max_pages=8)
+    cache = case.gpu(sgd)
+    for t in (cache.k, cache.v):
+        t.nan_to_num_(0.0)
+    sgd.pages_release(cache, ints([0, 64, 130]))
+    if taken:  # row 1 takes the pages
+        new, ws = sgd.pages_reserve(cache.with_lens(ints([0, 64, 130])), ints([0, 200, 0]))
+        assert sgd.workspace_status(ws) == 0 and new.tolist() == [0, 264, 130]
+        cache.lens[1] = 264
+        assert set(cache.page_table[1, 1:5].tolist()) & set(cache.page_table[0, :4].tolist())
+    k, v, L = cache.k.clone(), cache.v.clone(), cache.lens.tolist()
+
+    def go(held):
+        c = sgd.PagedKv(cache.k, cache.v, cache.page_table, cache.lens, cache.held if held else None, cache.ref_count)
+        if call == "keep":  # rows 1 and 2 keep everything
+            parts = [np.arange(1, 150), np.arange(L[1]), np.arange(L[2])]
+            cu = np.concatenate([[0], np.cumsum([len(p) for p in parts])])
+            return sgd.pages_keep(c, ints(np.tile(np.concatenate(parts), (2, 1))), ints(cu))
+        return sgd.pages_accept(c, ints([[3, 5, 6, -1, -1, -1, -1], [0, 1, 2, 3, 4, 5, 6], [0, 1, 2, 3, 4, 5, 6]]), ints([3, 7, 7]),
+                                ints([7, 7, 7]))
+
+    new, ws = go(True)
+    assert sgd.workspace_status(ws) == 0x4 and new.tolist() == L
+    assert torch.equal(cache.k, k) and torch.equal(cache.v, v)
+    if not taken:  # without held the free pages themselves tell
+        new, ws = go(False)
+        assert sgd.workspace_status(ws) == 0x8 and new.tolist() == L
+        assert torch.equal(cache.k, k) and torch.equal(cache.v, v)
