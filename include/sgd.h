@@ -546,7 +546,8 @@ int sgd_pages_release(const sgd_paged_kv *kv, const int32_t *keep, void *workspa
  * path     [B, M] int32; n_path, n_nodes [B] int32; new_lens [B] int32, not lens itself
  * Status: BAD_INDEX for a path that does not ascend or leaves the nodes (clamped) or a page outside
  * the pool, SIZE_MISMATCH for counts out of range (clamped), SHARED_PAGE for a row that would
- * write a shared page (left as it is, new_lens = lens).  A row that would write a page without
+ * write a shared page (left as it is, new_lens = lens; entries that stay where they are, up to the first
+ * that moves, are not written).  A row that would write a page without
  * references (BAD_INDEX) or is longer than its held pages (SIZE_MISMATCH; not checked where held is
  * NULL) is left as it is, too.
  */
@@ -560,7 +561,7 @@ int sgd_pages_accept(const sgd_paged_kv *kv, const int32_t *path, const int32_t 
  * idx      [Hkv, kept_total] int32, kept_total >= 1; cu_kept [B+1] int32; new_lens [B] int32, not
  *          lens itself
  * Status: BAD_INDEX and SHARED_PAGE as in sgd_pages_accept (a list that does not ascend or leaves the
- * row), SIZE_MISMATCH for a row whose range of cu_kept descends, leaves [0, kept_total] or is longer than
+ * row; the first token that moves in any head counts for all of them), SIZE_MISMATCH for a row whose range of cu_kept descends, leaves [0, kept_total] or is longer than
  * the row, or whose lens is out of range or more than its held pages (left as it is, new_lens = lens).
  * The pages that fell empty are given back by sgd_pages_release(kv, new_lens, ...).
  */

@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(PagedView k
     const int32_t *row = kv.table + (int64_t)b * kv.max_pages;
     // a row that was released but still has its old length lists pages that are free, or another row's by now
     if (kv.held && len > (int64_t)kv.held[b] * SGD_PAGE) return leave(SGD_STATUS_SIZE_MISMATCH);
-    // the pages written to: base / 64 .. (base + n - 1) / 64
+    // the pages of the entries that the list names: base / 64 .. (base + n - 1) / 64
     int shared = 0, vacant = 0;
     for (int j = base / SGD_PAGE + threadIdx.x; j < ceil_pages(base + n) && n > 0; j += kCompactThreads) {
         const int p = row[j];
@@ -368,8 +368,33 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(PagedView k
         else if (kv.ref[p] > 1) shared = 1;
         else if (kv.ref[p] < 1) vacant = 1;
     }
-    if (__syncthreads_or(shared)) return leave(SGD_STATUS_SHARED_PAGE);
     if (__syncthreads_or(vacant)) return leave(SGD_STATUS_BAD_INDEX);
+    int first = 0;  // entries before this one stay where they are
+    if (__syncthreads_or(shared)) {
+        // A shared page may hold entries that stay.  list ascends strictly, so those are its first ones; the row's heads
+        // agree on the first that moves in any of them.  Nothing before it is written, even where a list does not ascend.
+        __shared__ int32_t moves;
+        if (threadIdx.x == 0) moves = n;
+        __syncthreads();
+        for (int g = threadIdx.x; g < (ACCEPT ? 1 : kv.Hkv); g += kCompactThreads) {
+            const int32_t *of = list + (int64_t)(ACCEPT ? 0 : g - h) * a.kept_total;
+            int lo = 0, hi = n;
+            while (lo < hi) {
+                const int mid = (lo + hi) / 2;
+                if (of[mid] == mid) lo = mid + 1;
+                else hi = mid;
+            }
+            atomicMin(&moves, lo);
+        }
+        __syncthreads();
+        first = moves;
+        shared = 0;
+        for (int j = (base + first) / SGD_PAGE + threadIdx.x; j < ceil_pages(base + n) && first < n; j += kCompactThreads) {
+            const int p = row[j];
+            if (p >= 0 && p < kv.n_pages && kv.ref[p] > 1) shared = 1;
+        }
+        if (__syncthreads_or(shared)) return leave(SGD_STATUS_SHARED_PAGE);
+    }
     if (threadIdx.x == 0 && h == 0 && blockIdx.y == 0 && blockIdx.z == 0) a.new_lens[b] = base + n;
 
     extern __shared__ __align__(16) uint8_t smem[];
@@ -396,7 +421,7 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(PagedView k
         const int from = min(max(id, i), limit - 1);  // a bad list stays within [i, limit)
         if (from != id || prev >= id) bad |= SGD_STATUS_BAD_INDEX;
         int2 m = make_int2(-1, -1);
-        if (from != i) {
+        if (from != i && i >= first) {
             m = make_int2(pool_row(base + from), pool_row(base + i));
             if (m.y < 0) m.x = -1;
         }

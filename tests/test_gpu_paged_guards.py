@@ -72,3 +72,81 @@ def test_compaction_of_an_ended_row_writes_nothing(sgd, call, taken):
         new, ws = go(False)
         assert sgd.workspace_status(ws) == 0x8 and new.tolist() == L
         assert torch.equal(cache.k, k) and torch.equal(cache.v, v)
+
+
+def forked(sgd, L, seed):
+    """Row 0 of L tokens, row 1 its fork, row 2 with 300 tokens of its own; finite everywhere."""
+    case = Case((L, 0, 300), seed=seed, spare=4, max_pages=-(-L // PAGE) + 1)
+    case.k.nan_to_num_(0.0)
+    case.v.nan_to_num_(0.0)
+    cache, st = case.gpu(sgd), case.host()
+    sgd.pages_fork(cache, ints([0]), ints([1]))
+    assert st.fork(np.array([0]), np.array([1])) == 0
+    return cache, st
+
+
+def lists(per_row):
+    """per_row[b][h] -> (idx [Hkv, kept], cu)."""
+    cu = np.concatenate([[0], np.cumsum([len(r[0]) for r in per_row])]).astype(np.int32)
+    return np.stack([np.concatenate([r[h] for r in per_row]) for h in range(2)]).astype(np.int32), cu
+
+
+@pytest.mark.parametrize("L", [200, 5010, 192])
+def test_keep_of_shared_pages_that_are_not_written(sgd, L):
+    """Tokens that stay where they are in pages of a fork are no write: the row may drop others behind them."""
+    full = L // PAGE * PAGE
+    some = np.array([1, 5, 64, 130, 299])
+    cut = np.arange(100)                                                  # cut inside a shared page
+    own = [np.concatenate([np.arange(full), t]) for t in ([full + 1, full + 7], [full, full + 4])] if L > full else \
+        [np.arange(L)] * 2                                                # moves in the own last page alone
+    cache, st = forked(sgd, L, L)
+    idx, cu = lists([[cut, cut], own, [some, some + 0]])
+    new, ws = sgd.pages_keep(cache, ints(idx), ints(cu))
+    assert sgd.workspace_status(ws) == 0 and np.array_equal(new.cpu().numpy(), st.keep(idx, cu))
+    same_state(cache, st)
+    # one head would write a shared page: the row stays as it is, with all of its heads
+    cache, st = forked(sgd, L, L)
+    drop = np.delete(np.arange(len(own[0]) + 1), 70)
+    drop = drop[:len(own[0])] if drop[len(own[0]) - 1] < L else np.delete(np.arange(L), 70)
+    keep = [own[0][:len(drop)], drop]
+    idx, cu = lists([[cut, cut], keep, [some, some]])
+    new, ws = sgd.pages_keep(cache, ints(idx), ints(cu))
+    assert sgd.workspace_status(ws) == 0x40 and new.tolist() == [100, L, 5]
+    for h in range(2):
+        st._compact(2, h, 0, some)
+    same_state(cache, st)
+
+
+def test_keep_with_a_bad_list_writes_no_shared_page(sgd):
+    # entries in place around others out of order: whatever is made of such a list, the shared pages stay
+    for at, value in ((0, 5), (30, 2), (10, 190), (63, 64), (150, 149)):
+        cache, st = forked(sgd, 200, 3)
+        rows = np.arange(199)
+        rows[at] = value
+        idx, cu = lists([[rows, rows], [np.arange(200)] * 2, [np.arange(300)] * 2])
+        _, ws = sgd.pages_keep(cache, ints(idx), ints(cu))
+        assert sgd.workspace_status(ws) & 0x48
+        shared = st.ref > 1
+        for name in ("k", "v"):
+            got, want = getattr(cache, name).float().cpu().numpy(), getattr(st, name)
+            assert np.array_equal(got[shared], want[shared])
+
+
+def test_accept_of_shared_pages_that_are_not_written(sgd):
+    """A step's row forked before its drafts were accepted: nodes that stay where they are write nothing."""
+    n = M = 64
+    for path, ok in (([0, 1, 2], True), ([0, 2, 3], False), ([], True), (list(range(M)), True)):
+        cache, st = forked(sgd, 192, 9)
+        p = np.full((3, M), -1, np.int32)
+        p[0, :len(path)] = path
+        p[2, :2] = (1, 3)
+        n_path = np.array([len(path), 0, 2], np.int32)
+        n_nodes = np.array([n, 0, 5], np.int32)
+        new, ws = sgd.pages_accept(cache, ints(p), ints(n_path), ints(n_nodes))
+        if ok:
+            assert sgd.workspace_status(ws) == 0 and np.array_equal(new.cpu().numpy(), st.accept(p, n_path, n_nodes))
+        else:
+            assert sgd.workspace_status(ws) == 0x40 and new.tolist() == [192, 192, 297]
+            for h in range(2):
+                st._compact(2, h, 295, (1, 3))
+        same_state(cache, st)
