@@ -420,9 +420,10 @@ typedef struct {
     const float *v_scale;     /* I8: [1] */
     int32_t *page_table;      /* [B, max_pages] */
     int32_t *lens;            /* [B] */
-    int32_t *held;            /* [B]; needed by _reserve, _fork and _release; _accept and _keep check a row against it
-                               * where it is not NULL */
-    int32_t *ref_count;       /* [n_pages]; may be NULL for sgd_paged_attn and sgd_pages_append */
+    int32_t *held;            /* [B]; needed by _reserve, _fork and _release; _append, _accept and _keep check a row
+                               * against it where it is not NULL */
+    int32_t *ref_count;       /* [n_pages]; may be NULL for sgd_paged_attn and sgd_pages_append, which checks its
+                               * pages against it where it is not */
 } sgd_paged_kv;
 
 /* Workspace bytes for any of the calls that take an sgd_paged_kv: sgd_paged_attn with up to M query
@@ -503,12 +504,12 @@ int sgd_pages_reserve(const sgd_paged_kv *kv, const int32_t *add, int32_t *new_l
 /*
  * sgd_pages_append -- K and V of new tokens into the pages: of row b the tokens
  * cu_new[b] .. cu_new[b+1] - 1 of k_new and v_new become its last cu_new[b+1] - cu_new[b] entries
- * (lens[b] counts them already, as after sgd_pages_reserve, which refuses pages that another row
- * holds too; a row is not forked between the two calls).  An I8 cache takes their codes under
+ * (lens[b] counts them already, as after sgd_pages_reserve).  An I8 cache takes their codes under
  * its scales, as sgd_quantize_kv with SGD_SCHEME_B_CALIBRATED makes them.
  * k_new, v_new   [Hkv, T_new, D] BF16;  cu_new [B+1] int32, T_new = cu_new[B] (host value)
- * Status: BAD_INDEX for a page outside the pool, SIZE_MISMATCH for a token outside the row or a
- * cu_new that disagrees with T_new (those tokens are not written); BAD_SCALE.
+ * Status: BAD_INDEX for a page outside the pool or without references, SHARED_PAGE for one that another row
+ * holds too, SIZE_MISMATCH for a token outside the row and its held pages or a cu_new that disagrees with T_new
+ * (those tokens are not written); BAD_SCALE.
  */
 int sgd_pages_append(const sgd_paged_kv *kv, const void *k_new, const void *v_new, const int32_t *cu_new,
                      int64_t T_new, void *workspace, size_t workspace_bytes, void *stream);

@@ -150,7 +150,9 @@ int sgd_pages_append(const sgd_paged_kv *kv, const void *k_new, const void *v_ne
     if (rc != SGD_OK) return rc;
     if (!cu_new || (T_new > 0 && (!k_new || !v_new))) return SGD_ERR_NULL;
     if (T_new < 0 || T_new * kv->Hkv >= (int64_t(1) << 31)) return SGD_ERR_SHAPE;
-    if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(cu_new, 4)) return SGD_ERR_ALIGN;
+    if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(cu_new, 4) || !aligned(kv->held, 4) ||
+        !aligned(kv->ref_count, 4))
+        return SGD_ERR_ALIGN;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int sms;
     rc = begin(workspace, workspace_bytes, sizeof(WsHeader), true, s, &sms);

@@ -150,3 +150,46 @@ def test_accept_of_shared_pages_that_are_not_written(sgd):
             for h in range(2):
                 st._compact(2, h, 295, (1, 3))
         same_state(cache, st)
+
+
+# ---------------------------------------------------------------------------------------------
+# append
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "int8"])
+def test_append_writes_the_rows_own_pages_alone(sgd, dtype):
+    """Where lens does not count the new tokens (a reserve was refused) or the row has ended, the last entries lie in
+    pages that a fork shares, that are free, or that another row has taken: they stay as they are."""
+    rng = np.random.default_rng(3)
+    new = torch.from_numpy(rng.standard_normal((2, 70, 128), dtype=np.float32)).bfloat16().cuda()
+
+    def go(cache, cu, held=True, n=70):
+        c = sgd.PagedKv(cache.k, cache.v, cache.page_table, cache.lens, cache.held if held else None, cache.ref_count,
+                        cache.k_scale, cache.v_scale)
+        return sgd.workspace_status(sgd.pages_append(c, new[:, :n].contiguous(), new[:, :n].contiguous(), ints(cu)))
+
+    def make():
+        case = Case((200, 0, 64), seed=12, spare=4, max_pages=8, dtype=dtype)
+        case.k, case.v = (t.nan_to_num(0.0) if dtype == "bf16" else t for t in (case.k, case.v))
+        return case.gpu(sgd)
+
+    # 200 tokens forked: the last 8 in a page of their own, 62 of the 70 in a shared one
+    cache = make()
+    sgd.pages_fork(cache, ints([0]), ints([1]))
+    k = cache.k.clone()
+    assert go(cache, [0, 70, 70, 70]) == 0x40
+    changed = (cache.k != k).flatten(1).any(1).nonzero()[:, 0].tolist()
+    assert changed == [int(cache.page_table[0, 3])] and (cache.k[changed[0], :, 8:] == k[changed[0], :, 8:]).all()
+    # an ended row, its pages free
+    cache = make()
+    sgd.pages_release(cache, ints([0, 0, 64]))
+    k, v = cache.k.clone(), cache.v.clone()
+    assert go(cache, [0, 70, 70, 70]) == 0x4 and torch.equal(cache.k, k) and torch.equal(cache.v, v)
+    assert go(cache, [0, 70, 70, 70], held=False) == 0x8 and torch.equal(cache.k, k) and torch.equal(cache.v, v)
+    # taken by row 2
+    _, ws = sgd.pages_reserve(cache.with_lens(ints([0, 0, 64])), ints([0, 0, 250]))
+    assert sgd.workspace_status(ws) == 0
+    assert go(cache, [0, 70, 70, 70]) == 0x4 and torch.equal(cache.k, k) and torch.equal(cache.v, v)
+    # without the counts a caller answers for the pages
+    cache = make()
+    c = sgd.PagedKv(cache.k, cache.v, cache.page_table, cache.lens, k_scale=cache.k_scale, v_scale=cache.v_scale)
+    assert sgd.workspace_status(sgd.pages_append(c, new, new, ints([0, 70, 70, 70]))) == 0
