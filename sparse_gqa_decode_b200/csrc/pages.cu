@@ -334,10 +334,33 @@ struct CompactShared {
     int2 move[kRing + 1][kCompactThreads];      // their (from, to) as rows of the pool; from < 0: stays
 };
 
+// The first of n entries that moves in any of a row's `heads` lists, `stride` apart: one that names itself stays, and as
+// a list ascends strictly those are its first ones.  `least` is shared memory.  Out of line: it is for rows with
+// shared pages alone, and its code beside the copies' cost the others 2 of 52 us (8 x 32K tokens kept to an eighth).
+__device__ __noinline__ int first_move(const int32_t *lists, int heads, int64_t stride, int n, int32_t *least) {
+    if (threadIdx.x == 0) *least = n;
+    __syncthreads();
+    for (int g = threadIdx.x; g < heads; g += kCompactThreads) {
+        const int32_t *list = lists + g * stride;
+        int lo = 0, hi = n;
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (list[mid] == mid) lo = mid + 1;
+            else hi = mid;
+        }
+        atomicMin(least, lo);
+    }
+    __syncthreads();
+    const int first = *least;
+    __syncthreads();  // before the memory serves another purpose
+    return first;
+}
+
 template <bool ACCEPT, int LANES>
 __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(PagedView kv, CompactArgs a) {
     const int b = blockIdx.x / kv.Hkv, h = blockIdx.x % kv.Hkv;
     int L = kv.lens[b], bad = 0, n, base = 0, limit;
+    const int held = kv.held ? kv.held[b] : kv.max_pages;
     const int32_t *list;
     auto leave = [&](int why) {  // the row stays as it is, and a release that follows takes nothing from it
         if (threadIdx.x != 0) return;
@@ -362,35 +385,25 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(PagedView k
     }
     const int32_t *row = kv.table + (int64_t)b * kv.max_pages;
     // a row that was released but still has its old length lists pages that are free, or another row's by now
-    if (kv.held && len > (int64_t)kv.held[b] * SGD_PAGE) return leave(SGD_STATUS_SIZE_MISMATCH);
+    if (len > (int64_t)held * SGD_PAGE) return leave(SGD_STATUS_SIZE_MISMATCH);
     // the pages of the entries that the list names: base / 64 .. (base + n - 1) / 64
     int shared = 0, vacant = 0;
     for (int j = base / SGD_PAGE + threadIdx.x; j < ceil_pages(base + n) && n > 0; j += kCompactThreads) {
         const int p = row[j];
-        if (p < 0 || p >= kv.n_pages) bad |= SGD_STATUS_BAD_INDEX;
-        else if (kv.ref[p] > 1) shared = 1;
-        else if (kv.ref[p] < 1) vacant = 1;
-    }
-    if (__syncthreads_or(vacant)) return leave(SGD_STATUS_BAD_INDEX);
-    int first = 0;  // entries before this one stay where they are
-    if (__syncthreads_or(shared)) {
-        // A shared page may hold entries that stay.  list ascends strictly, so those are its first ones; the row's heads
-        // agree on the first that moves in any of them.  Nothing before it is written, even where a list does not ascend.
-        __shared__ int32_t moves;
-        if (threadIdx.x == 0) moves = n;
-        __syncthreads();
-        for (int g = threadIdx.x; g < (ACCEPT ? 1 : kv.Hkv); g += kCompactThreads) {
-            const int32_t *of = list + (int64_t)(ACCEPT ? 0 : g - h) * a.kept_total;
-            int lo = 0, hi = n;
-            while (lo < hi) {
-                const int mid = (lo + hi) / 2;
-                if (of[mid] == mid) lo = mid + 1;
-                else hi = mid;
-            }
-            atomicMin(&moves, lo);
+        if (p < 0 || p >= kv.n_pages) {
+            bad |= SGD_STATUS_BAD_INDEX;
+        } else {
+            const int owners = kv.ref[p];
+            shared |= owners > 1;
+            vacant |= owners < 1;
         }
-        __syncthreads();
-        first = moves;
+    }
+    extern __shared__ __align__(16) uint8_t smem[];
+    auto &sh = *reinterpret_cast<CompactShared<LANES> *>(smem);
+    int first = 0;  // entries before this one stay where they are
+    if (__syncthreads_or(shared | vacant)) {
+        if (__syncthreads_or(vacant)) return leave(SGD_STATUS_BAD_INDEX);
+        first = first_move(ACCEPT ? list : list - (int64_t)h * a.kept_total, ACCEPT ? 1 : kv.Hkv, a.kept_total, n, &sh.ids[0][0]);
         shared = 0;
         for (int j = (base + first) / SGD_PAGE + threadIdx.x; j < ceil_pages(base + n) && first < n; j += kCompactThreads) {
             const int p = row[j];
@@ -400,8 +413,6 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(PagedView k
     }
     if (threadIdx.x == 0 && h == 0 && blockIdx.y == 0 && blockIdx.z == 0) a.new_lens[b] = base + n;
 
-    extern __shared__ __align__(16) uint8_t smem[];
-    auto &sh = *reinterpret_cast<CompactShared<LANES> *>(smem);
     constexpr int ROWS = kCompactThreads;  // of a step
     const int row_bytes = kv.D * kv.es, tid = threadIdx.x;
     uint8_t *pool = static_cast<uint8_t *>(blockIdx.y ? kv.v : kv.k) + (int64_t)blockIdx.z * LANES * 16 + tid % LANES * 16;
