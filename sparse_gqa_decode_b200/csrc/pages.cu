@@ -271,14 +271,15 @@ __global__ void __launch_bounds__(256) append_kernel(PagedView kv, const __nv_bf
                 else hi = mid - 1;
             }
             const int64_t t = (int64_t)kv.lens[lo] - cu[lo + 1] + i;
-            if (i < cu[lo] || i >= cu[lo + 1] || t < 0 || t >= (int64_t)(kv.held ? kv.held[lo] : kv.max_pages) * SGD_PAGE ||
-                t >= (int64_t)kv.max_pages * SGD_PAGE) {
+            if (i < cu[lo] || i >= cu[lo + 1] || t < 0 || t >= (int64_t)kv.max_pages * SGD_PAGE) {
                 bad = SGD_STATUS_SIZE_MISMATCH;
             } else {
                 const int p = kv.table[(int64_t)lo * kv.max_pages + t / SGD_PAGE];
+                const int held = kv.held ? kv.held[lo] : kv.max_pages;
                 // a page of the row's own: lens may be that of a refused reserve, or of a row that has ended
                 const int owners = p < 0 || p >= kv.n_pages ? 0 : kv.ref ? kv.ref[p] : 1;
-                if (owners == 1) row = ((int64_t)p * kv.Hkv + h) * SGD_PAGE + t % SGD_PAGE;
+                if (t >= (int64_t)held * SGD_PAGE) bad = SGD_STATUS_SIZE_MISMATCH;
+                else if (owners == 1) row = ((int64_t)p * kv.Hkv + h) * SGD_PAGE + t % SGD_PAGE;
                 else bad = owners < 1 ? SGD_STATUS_BAD_INDEX : SGD_STATUS_SHARED_PAGE;
             }
         }
