@@ -156,7 +156,7 @@ int sgd_pages_append(const sgd_paged_kv *kv, const void *k_new, const void *v_ne
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int sms;
     rc = begin(workspace, workspace_bytes, sizeof(WsHeader), true, s, &sms);
-    if (rc != SGD_OK || T_new == 0) return rc;
+    if (rc != SGD_OK) return rc;
     return launch_pages_append(view(kv), k_new, v_new, cu_new, T_new, status_of(workspace), s);
 }
 

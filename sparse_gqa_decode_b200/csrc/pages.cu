@@ -4,6 +4,8 @@
 // The pool's whole allocation state is ref_count: a page is free when its count is 0, and the
 // lowest free page is taken first.  So the calls keep no list whose order could depend on how threads
 // ran: equal states give equal pages, and releasing what was just taken restores the state exactly.
+#include <algorithm>
+
 #include "paged.h"
 #include "quant.cuh"
 #include "scan.cuh"
@@ -526,7 +528,8 @@ int launch_pages_release(const PagedView &kv, const int32_t *keep, int32_t *stat
 
 int launch_pages_append(const PagedView &kv, const void *k_new, const void *v_new, const int32_t *cu, int64_t T_new,
                         int32_t *status, cudaStream_t s) {
-    const dim3 grid((unsigned)((T_new + kAppendTokens - 1) / kAppendTokens), kv.Hkv);
+    // without tokens one CTA still checks cu_new
+    const dim3 grid((unsigned)std::max<int64_t>((T_new + kAppendTokens - 1) / kAppendTokens, 1), kv.Hkv);
     auto k = kv.es == 1 ? append_kernel<true> : append_kernel<false>;
     launch_k(k, grid, dim3(256), 0, s, 1, kv, static_cast<const __nv_bfloat16 *>(k_new),
              static_cast<const __nv_bfloat16 *>(v_new), cu, T_new, status);

@@ -193,3 +193,10 @@ def test_append_writes_the_rows_own_pages_alone(sgd, dtype):
     cache = make()
     c = sgd.PagedKv(cache.k, cache.v, cache.page_table, cache.lens, k_scale=cache.k_scale, v_scale=cache.v_scale)
     assert sgd.workspace_status(sgd.pages_append(c, new, new, ints([0, 70, 70, 70]))) == 0
+
+
+def test_append_of_nothing_checks_its_offsets(sgd):
+    cache = Case((100, 70), seed=4).gpu(sgd)
+    none = torch.zeros(2, 0, 128, dtype=torch.bfloat16, device="cuda")
+    for cu, code in (([0, 0, 0], 0), ([0, 3, 6], 0x4), ([0, 1, 0], 0), ([1, 1, 1], 0x4)):
+        assert sgd.workspace_status(sgd.pages_append(cache, none, none, ints(cu))) == code, cu
