@@ -1055,7 +1055,8 @@ int launch(const PagedView &kv, const PagedAttnArgs &a, const AttnPlan &plan, cu
 
 size_t paged_attn_scratch(int B, int Hkv, int D, int G, int M, int sms) {
     const Shape sh(G, M);
-    const size_t slots = (size_t)sh.ranges(sms) * sh.RT * 2 * sh.rows();
+    // as many CTAs as SMs, though RT may not divide them: a smaller step's RT may, and takes the same workspace
+    const size_t slots = (size_t)std::max(sms, sh.RT) * 2 * sh.rows();
     return up256(slots * D * 4) + up256(slots * 4) + up256((size_t)B * Hkv * 8) + up256((size_t)sms * 4);
 }
 

@@ -1,0 +1,28 @@
+"""Host side of the paged calls: sizes and arguments at the ends of their ranges, without a GPU."""
+import ctypes
+
+import pytest
+
+from test_paged_cpu import ALL_OK, _kv, calls, sgd  # noqa: F401
+
+
+@pytest.mark.parametrize("D,dtype", [(128, 1), (64, 2)])
+def test_a_workspace_serves_every_smaller_step(sgd, D, dtype):
+    """sgd_paged_workspace_size promises bytes for up to M query tokens and G heads."""
+    assert (sgd.SGD_BF16, sgd.SGD_I8) == (1, 2)
+    kv = _kv(sgd, B=4, D=D, dtype=dtype, k_scale=0x50000, v_scale=0x50010)
+    size = {(G, M): sgd.lib.sgd_paged_workspace_size(ctypes.byref(kv), G, M) for G in range(1, 17) for M in range(65)}
+    assert all(size.values())
+    for G in range(1, 17):
+        for M in range(1, 65):
+            assert size[G, M - 1] <= size[G, M], (G, M)
+            assert G == 1 or size[G - 1, M] <= size[G, M], (G, M)
+
+
+def test_narrower_steps_run_on_the_widest_steps_workspace(sgd):
+    kv, attn = _kv(sgd, B=4), calls(sgd)["attn"]
+    for G, M in ((16, 40), (9, 64), (12, 60), (8, 64)):
+        n = sgd.lib.sgd_paged_workspace_size(ctypes.byref(kv), G, M)
+        for g in range(1, G + 1):
+            for m in range(1, M + 1):
+                assert attn(kv, n=n, G=g, M=m) not in ALL_OK, (G, M, g, m)
