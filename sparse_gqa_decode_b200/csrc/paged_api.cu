@@ -149,7 +149,7 @@ int sgd_pages_append(const sgd_paged_kv *kv, const void *k_new, const void *v_ne
     int rc = check_paged(kv, false);
     if (rc != SGD_OK) return rc;
     if (!cu_new || (T_new > 0 && (!k_new || !v_new))) return SGD_ERR_NULL;
-    if (T_new < 0 || T_new * kv->Hkv >= (int64_t(1) << 31)) return SGD_ERR_SHAPE;
+    if (T_new < 0 || T_new >= (int64_t(1) << 31) || T_new * kv->Hkv >= (int64_t(1) << 31)) return SGD_ERR_SHAPE;
     if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(cu_new, 4) || !aligned(kv->held, 4) ||
         !aligned(kv->ref_count, 4))
         return SGD_ERR_ALIGN;

@@ -26,3 +26,10 @@ def test_narrower_steps_run_on_the_widest_steps_workspace(sgd):
         for g in range(1, G + 1):
             for m in range(1, M + 1):
                 assert attn(kv, n=n, G=g, M=m) not in ALL_OK, (G, M, g, m)
+
+
+def test_append_refuses_counts_beyond_32_bits(sgd):
+    # T_new * Hkv wraps to 0 and to negative numbers in 64 bits
+    for Hkv, T in ((2, 1 << 62), (2, 1 << 63 - 1), (4, 1 << 62), (2, (1 << 63) - 1), (2, 1 << 30), (1, 1 << 31)):
+        assert calls(sgd)["append"](_kv(sgd, Hkv=Hkv), T=T) == -2, (Hkv, T)
+    assert calls(sgd)["append"](_kv(sgd), T=(1 << 30) - 1) not in ALL_OK
