@@ -644,7 +644,9 @@ class _On:
     the call may still run."""
 
     def __init__(self, device, stream):
-        if device.type == "cuda" and device.index != torch.cuda.current_device():
+        if device.type != "cuda":
+            raise ValueError(f"the tensors are on {device}, not on a CUDA device")
+        if device.index != torch.cuda.current_device():
             raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
         self.device, self.stream = device, stream
         self.raw = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
