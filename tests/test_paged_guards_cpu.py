@@ -50,7 +50,7 @@ def test_binding_refuses_tensors_that_are_not_on_a_gpu(sgd):
         lambda: sgd.verify_tree(torch.zeros(3, 2, 8), table, table, u, u[:, 0].contiguous(), out=(out, table, lens), workspace=ws,
                                 stream=stream),
         lambda: sgd.pages_reserve(cache, lens, out=out, workspace=ws, stream=stream),
-        lambda: sgd.pages_append(cache, k[:2, 0], k[:2, 0], cu, workspace=ws, stream=stream),
+        lambda: sgd.pages_append(cache, k[0], k[0], cu, workspace=ws, stream=stream),
         lambda: sgd.pages_fork(cache, lens[:1], lens[1:2], workspace=ws, stream=stream),
         lambda: sgd.pages_release(cache, lens, workspace=ws, stream=stream),
         lambda: sgd.pages_accept(cache, table, lens, lens, out=out, workspace=ws, stream=stream),
