@@ -665,6 +665,11 @@ class _On:
         return workspace
 
 
+def _int32(n: int) -> int:
+    """The nearest 32-bit number: what lies beyond either end means the same to the call, or is refused like it."""
+    return max(min(n, 2 ** 31 - 1), -2 ** 31)
+
+
 def _nbytes(t) -> int:
     return t.numel() * t.element_size()
 
@@ -694,9 +699,8 @@ def paged_attn(q: torch.Tensor, G: int, cache: PagedKv, parent=None, n_nodes=Non
         _want(lse, "lse", torch.float32, (cache.B, M, Hq), dev)
     ws = on.workspace(0 if workspace is not None else paged_workspace_size(cache, G, M), workspace)
     _check(lib.sgd_paged_attn(q.data_ptr(), G, M, cache._ref, None if parent is None else parent.data_ptr(),
-                              None if n_nodes is None else n_nodes.data_ptr(), min(window, 2 ** 31 - 1),
-                              min(sinks, 2 ** 31 - 1), o.data_ptr(),
-                              lse.data_ptr(), ws.data_ptr(), _nbytes(ws), on.raw), "sgd_paged_attn")
+                              None if n_nodes is None else n_nodes.data_ptr(), _int32(window),
+                              _int32(sinks), o.data_ptr(), lse.data_ptr(), ws.data_ptr(), _nbytes(ws), on.raw), "sgd_paged_attn")
     return o, lse, ws
 
 

@@ -58,3 +58,22 @@ def test_binding_refuses_tensors_that_are_not_on_a_gpu(sgd):
     ):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_binding_keeps_the_sign_of_a_window(sgd, monkeypatch):
+    """A number below -2^31 wraps on its way into 32 bits, to 0 (no window at all) or to a positive one."""
+    import types
+
+    import torch
+    k = torch.zeros(1, 1, 64, 64, dtype=torch.bfloat16)
+    table = torch.zeros(1, 1, dtype=torch.int32)
+    cache = sgd.PagedKv(k, k, table, table[0])
+    q = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16)
+    host = types.SimpleNamespace(raw=0, empty=lambda shape, dtype: torch.empty(shape, dtype=dtype),
+                                 workspace=lambda n, ws: ws)
+    monkeypatch.setattr(sgd, "_On", lambda device, stream: host)
+    ws = torch.zeros(1 << 26, dtype=torch.uint8)
+    for n in (-1, -2 ** 31, -2 ** 31 - 1, -2 ** 32, -2 ** 32 + 1, -2 ** 40):
+        for kw in (dict(window=n), dict(window=5, sinks=n)):
+            with pytest.raises(sgd.SgdError, match=r"sgd_paged_attn.*-8"):
+                sgd.paged_attn(q, 1, cache, workspace=ws, **kw)
