@@ -80,7 +80,8 @@ inline cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_
 }
 
 // A launch that may begin while the stream's last kernel is still ending: `kern` calls grid_dependency_wait() before
-// it touches anything that kernel writes (or reads, where `kern` writes it).
+// it touches anything that kernel writes (or reads, where `kern` writes it).  Its pointers are plain ones: a load
+// through __restrict__ or __ldg is taken for one of data that never changes, and may move in front of the wait.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_k_early(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                                   Args &&...args) {

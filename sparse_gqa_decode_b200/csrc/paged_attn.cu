@@ -549,8 +549,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             float scale = a.scale_log2, vs = 1.f, scale_k = scale;
             if constexpr (C::I8) {
                 const bool report = blockIdx.x == 0 && g == 0 && r == 0;
-                scale_k *= calibrated_scale(kv.k_scale, &bar.status, report);
-                vs = calibrated_scale(kv.v_scale, &bar.status, report);
+                scale_k *= checked_scale(*kv.k_scale, &bar.status, report);
+                vs = checked_scale(*kv.v_scale, &bar.status, report);
             }
             uint32_t at = 0, seg = 0, ns = 0, nv = 0, no[2] = {0, 0};
             float2 *ml = reinterpret_cast<float2 *>(smem + C::OFF_ML);

@@ -22,7 +22,7 @@ __device__ __forceinline__ int ceil_pages(int tokens) { return (tokens + SGD_PAG
 // Called by every thread of the block.  One pass over ref_count, 4 entries per thread and round,
 // that ends as soon as enough are found: 16 KB a round, about a microsecond each (the CTA waits for
 // one round of loads and one block scan).
-__device__ int find_free(const int32_t *__restrict__ ref, int n_pages, int want, int32_t *list, int32_t *sm) {
+__device__ int find_free(const int32_t *ref, int n_pages, int want, int32_t *list, int32_t *sm) {
     int found = 0;
     for (int at = 0; at < n_pages && found < want; at += kAllocThreads * 4) {
         const int p0 = at + threadIdx.x * 4;
@@ -72,7 +72,7 @@ __device__ __forceinline__ int owner(const int32_t *off, int n, int r) {
 
 // One CTA: needs, checks, the free pages, then the new state.  Everything is decided before
 // anything is written.
-__global__ void __launch_bounds__(kAllocThreads) reserve_kernel(PagedView kv, const int32_t *__restrict__ add,
+__global__ void __launch_bounds__(kAllocThreads) reserve_kernel(PagedView kv, const int32_t *add,
                                                                 int32_t *new_lens, int32_t *off, int32_t *list,
                                                                 int32_t *status) {
     __shared__ int32_t sm[33];
@@ -132,8 +132,8 @@ __global__ void __launch_bounds__(kAllocThreads) reserve_kernel(PagedView kv, co
 
 // One CTA: checks the rows of a fork and takes the pages for part-filled last pages.
 // fresh[i]: the new page of fork i, -1 where none is needed; *go = 1 where the fork goes ahead.
-__global__ void __launch_bounds__(kAllocThreads) fork_plan_kernel(PagedView kv, const int32_t *__restrict__ src,
-                                                                  const int32_t *__restrict__ dst, int n,
+__global__ void __launch_bounds__(kAllocThreads) fork_plan_kernel(PagedView kv, const int32_t *src,
+                                                                  const int32_t *dst, int n,
                                                                   int32_t *mark, int32_t *fresh, int32_t *list,
                                                                   int32_t *go, int32_t *status) {
     __shared__ int32_t sm[33];
@@ -184,10 +184,8 @@ __global__ void __launch_bounds__(kAllocThreads) fork_plan_kernel(PagedView kv, 
 // CTA (i, h, K or V): the valid tokens of fork i's part-filled page, one KV head of K or V (one
 // contiguous run of at most 16 KB); the CTA of h = 0, K also writes the new row's state.  A release and a fork of
 // 64 rows to 7 each: 24 us, of which the plan takes 8 and the copies 16.
-__global__ void __launch_bounds__(128) fork_copy_kernel(PagedView kv, const int32_t *__restrict__ src,
-                                                        const int32_t *__restrict__ dst,
-                                                        const int32_t *__restrict__ fresh,
-                                                        const int32_t *__restrict__ go, int32_t *status) {
+__global__ void __launch_bounds__(128) fork_copy_kernel(PagedView kv, const int32_t *src, const int32_t *dst,
+                                                        const int32_t *fresh, const int32_t *go, int32_t *status) {
     grid_dependency_wait();
     if (*go == 0) return;
     const int i = blockIdx.x, h = blockIdx.y, s = src[i], d = dst[i];

@@ -119,11 +119,14 @@ __device__ __forceinline__ uint32_t codes4_sat(const float *x, float s, float r,
 
 // A calibrated per-tensor scale as read by every thread: a negative or non-finite value counts as
 // zero (zero codes) and, where `report`, sets SGD_STATUS_BAD_SCALE.
-__device__ __forceinline__ float calibrated_scale(const float *p, int32_t *status, bool report) {
-    const float s = __ldg(p);
+__device__ __forceinline__ float checked_scale(float s, int32_t *status, bool report) {
     if (s >= 0.f && s <= 3.402823466e38f) return s;
     if (report) atomicOr(status, SGD_STATUS_BAD_SCALE);
     return 0.f;
+}
+
+__device__ __forceinline__ float calibrated_scale(const float *p, int32_t *status, bool report) {
+    return checked_scale(__ldg(p), status, report);
 }
 
 template <int VE, bool SAT = false>

@@ -77,3 +77,28 @@ def test_binding_keeps_the_sign_of_a_window(sgd, monkeypatch):
         for kw in (dict(window=n), dict(window=5, sinks=n)):
             with pytest.raises(sgd.SgdError, match=r"sgd_paged_attn.*-8"):
                 sgd.paged_attn(q, 1, cache, workspace=ws, **kw)
+
+
+def kernels_that_wait():
+    """(name, parameters, body) of each kernel that is launched early and waits for the stream's last one."""
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sparse_gqa_decode_b200", "csrc")
+    for name in sorted(os.listdir(csrc)):
+        if name.endswith(".cu"):
+            text = open(os.path.join(csrc, name)).read()
+            for part in text.split("__global__ void")[1:]:
+                m = re.match(r"(?:\s|__launch_bounds__\([^)]*\))*(\w+)\((.*?)\) \{\n(.*?)\n\}\n", part, re.S)
+                if m and "grid_dependency_wait()" in m.group(3):
+                    yield m.groups()
+
+
+def test_early_kernels_promise_nothing_about_their_inputs(sgd):
+    """What the stream's last kernel writes is not read-only while an early kernel runs: __restrict__ on a const
+    pointer and __ldg say that it is, and such a load may move in front of the wait."""
+    found = {name: (args, body) for name, args, body in kernels_that_wait()}
+    assert set(found) == {"paged_attn_kernel", "paged_merge_kernel", "reserve_kernel", "fork_plan_kernel", "fork_copy_kernel"}
+    for name, (args, body) in found.items():
+        assert "__restrict__" not in args, name
+        for word in ("__ldg(", "calibrated_scale(", ".nc"):
+            assert word not in body, (name, word)
