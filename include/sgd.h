@@ -450,8 +450,8 @@ size_t sgd_paged_workspace_size(const sgd_paged_kv *kv, int G, int M);
  * K and V of an entry that no query of the sequence sees may be anything; those of an entry that
  * some query sees must be finite.  A query with a NaN gets NaN, alone.  B * Hkv * (max_pages / 2 + 4)
  * stays below 2^31 (SGD_ERR_SHAPE).
- * Status: BAD_INDEX for a page outside the pool (page 0 is read), a parent outside [-1, m) (taken
- * as -1) or n_nodes outside [0, M] (clamped); SIZE_MISMATCH for lens[b] outside
+ * Status: BAD_INDEX for a page outside the pool of which a query sees an entry (page 0 is read; the
+ * page table entries of other pages may be anything), a parent outside [-1, m) (taken as -1) or n_nodes outside [0, M] (clamped); SIZE_MISMATCH for lens[b] outside
  * [0, 64 * max_pages] (clamped); BAD_SCALE as in sgd_quantize_kv.
  */
 int sgd_paged_attn(const void *q, int G, int M, const sgd_paged_kv *kv, const int32_t *parent,

@@ -383,7 +383,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 for (int i = 0; i < np; ++i) {
                     int p = row[p0 + i];
                     if (p < 0 || p >= kv.n_pages) {
-                        bad = SGD_STATUS_BAD_INDEX;
+                        // an error where a query sees an entry of the page; one between the first tokens and the windows may
+                        // have been given back
+                        const int t = (p0 + i) * SGD_PAGE;
+                        if (w.s.n > 0 && !(a.window && t >= a.sinks && t + SGD_PAGE <= w.s.win)) bad = SGD_STATUS_BAD_INDEX;
                         p = 0;
                     }
                     const int y = (p * kv.Hkv + w.h) * SGD_PAGE;

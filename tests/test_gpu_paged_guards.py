@@ -200,3 +200,40 @@ def test_append_of_nothing_checks_its_offsets(sgd):
     none = torch.zeros(2, 0, 128, dtype=torch.bfloat16, device="cuda")
     for cu, code in (([0, 0, 0], 0), ([0, 3, 6], 0x4), ([0, 1, 0], 0), ([1, 1, 1], 0x4)):
         assert sgd.workspace_status(sgd.pages_append(cache, none, none, ints(cu))) == code, cu
+
+
+# ---------------------------------------------------------------------------------------------
+# attention
+# ---------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "int8"])
+@pytest.mark.parametrize("M", [3, 40])
+def test_attn_asks_nothing_of_pages_that_no_query_sees(sgd, dtype, M):
+    """Table entries between the first tokens and the window may hold anything, beside seen pages too."""
+    lens, window, sinks = (700, 130, 901, 1500), 70, 5
+    case = Case(lens, dtype=dtype, seed=9)
+    q = case.query(M, 8).cuda()
+    want = sgd.paged_attn(q, 8, case.gpu(sgd), window=window, sinks=sinks)
+    assert sgd.workspace_status(want[2]) == 0
+    gone, seen = 0, []
+    for b, L in enumerate(lens):
+        first = max(L - M + 1 - window, 0)  # the first entry of any window
+        for j in range(-(-L // PAGE)):
+            if j * PAGE >= sinks and (j + 1) * PAGE <= first:
+                case.table[b, j] = (-1, case.n_pages, 2 ** 31 - 1)[gone % 3]
+                gone += 1
+            else:
+                seen.append((b, j))
+    assert gone > 25
+    got = sgd.paged_attn(q, 8, case.gpu(sgd), window=window, sinks=sinks)
+    assert sgd.workspace_status(got[2]) == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # a row without nodes sees nothing at all
+    n = ints([M, 0, M, M])
+    bare = case.gpu(sgd)
+    bare.page_table[1] = -1
+    got = sgd.paged_attn(q, 8, bare, n_nodes=n, window=window, sinks=sinks)
+    assert sgd.workspace_status(got[2]) == 0 and (got[0][1] == 0).all() and torch.isneginf(got[1][1]).all()
+    for b, j in seen:  # every other one counts
+        cache = case.gpu(sgd)
+        cache.page_table[b, j] = -1
+        assert sgd.workspace_status(sgd.paged_attn(q, 8, cache, window=window, sinks=sinks)[2]) == 0x8, (b, j)
