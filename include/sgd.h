@@ -394,6 +394,10 @@ int sgd_decode_attn_noalloc(const void *q, sgd_dtype q_dtype, int G, const sgd_k
  * verify_tree accepts drafted tokens, pages_accept keeps the accepted ones, pages_fork,
  * pages_keep and pages_release branch, cut and end sequences.  All state is in device memory
  * and every call is stream-ordered, so a whole step runs, and is captured, without the host.
+ * Where pages_reserve may refuse (NO_PAGES), such a step takes its counts on the device from what was
+ * granted: n_nodes[b] = new_lens[b] - lens[b] (new_lens a tensor of its own), cu_new their running sum.  They are 0 after a refusal,
+ * and the calls that follow change nothing.  With counts of its own it would take each row's last tokens
+ * for the step's: written over by pages_append, dropped by pages_accept.
  * The pages have no counterpart to these entry points ([CD] names speculative decoding, [NSA]
  * section 2.1 reads the cache by 64-token blocks).
  *
@@ -495,7 +499,8 @@ int sgd_verify_tree(const void *p, sgd_dtype p_dtype, const void *q, int B, int 
  * suffice, SIZE_MISMATCH where a row would pass max_pages or add, lens or held is out of range,
  * SHARED_PAGE where a row would grow inside a page that another row holds too (a row cut back in
  * pages that it shares gives those behind its end back first: sgd_pages_release), BAD_INDEX where
- * a held page that it would grow in is outside the pool.
+ * a held page that it would grow in is outside the pool.  The calls that follow know of a refusal by their
+ * counts alone (see above).
  * add      [B] int32, >= 0;  new_lens [B] int32 (may be lens itself)
  */
 int sgd_pages_reserve(const sgd_paged_kv *kv, const int32_t *add, int32_t *new_lens, void *workspace,
@@ -504,7 +509,7 @@ int sgd_pages_reserve(const sgd_paged_kv *kv, const int32_t *add, int32_t *new_l
 /*
  * sgd_pages_append -- K and V of new tokens into the pages: of row b the tokens
  * cu_new[b] .. cu_new[b+1] - 1 of k_new and v_new become its last cu_new[b+1] - cu_new[b] entries
- * (lens[b] counts them already, as after sgd_pages_reserve).  An I8 cache takes their codes under
+ * (lens[b] counts them already, as after a sgd_pages_reserve that was not refused).  An I8 cache takes their codes under
  * its scales, as sgd_quantize_kv with SGD_SCHEME_B_CALIBRATED makes them.
  * k_new, v_new   [Hkv, T_new, D] BF16;  cu_new [B+1] int32, T_new = cu_new[B] (host value)
  * Status: BAD_INDEX for a page outside the pool or without references, SHARED_PAGE for one that another row

@@ -22,6 +22,8 @@ Variants: ``oam_select`` on a bf16/f32 cache or on the INT8 cache with stored va
 A speculative step over a paged cache (``PagedKv``; all state stays on the device)::
 
     grown, _ = pages_reserve(cache, n_nodes)              # room for the step's nodes
+    n_nodes = grown - cache.lens                          # 0 everywhere if the pool had too few pages
+    cu_new = torch.nn.functional.pad(n_nodes.cumsum(0, dtype=torch.int32), (1, 0))
     step = cache.with_lens(grown)
     pages_append(step, k_new, v_new, cu_new)              # their keys and values
     out, lse, _ = paged_attn(q, G, step, parent=parent, n_nodes=n_nodes, window=0, sinks=0)
@@ -749,7 +751,8 @@ def _paged_ws(on: _On, cache: PagedKv, workspace):
 
 
 def pages_reserve(cache: PagedKv, add: torch.Tensor, out=None, workspace=None, stream=None):
-    """Pages for ``add`` int32 [B] more tokens of each row.  Returns (new_lens [B], ws)."""
+    """Pages for ``add`` int32 [B] more tokens of each row.  Returns (new_lens [B], ws); new_lens is cache.lens where
+    the call was refused (its status says why), so that new_lens - cache.lens is what was granted."""
     _want(add, "add", torch.int32, (cache.B,), cache.device)
     on = _On(cache.device, stream)
     new, ws = _new_lens(on, cache, out), _paged_ws(on, cache, workspace)

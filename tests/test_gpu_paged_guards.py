@@ -237,3 +237,34 @@ def test_attn_asks_nothing_of_pages_that_no_query_sees(sgd, dtype, M):
         cache = case.gpu(sgd)
         cache.page_table[b, j] = -1
         assert sgd.workspace_status(sgd.paged_attn(q, 8, cache, window=window, sinks=sinks)[2]) == 0x8, (b, j)
+
+
+# ---------------------------------------------------------------------------------------------
+# together
+# ---------------------------------------------------------------------------------------------
+def test_a_step_whose_reserve_was_refused_changes_nothing(sgd):
+    """The step's counts taken from what the reserve granted, on the device: where the pool has too few pages the calls
+    that follow write, answer and accept nothing."""
+    B, M, Hkv, G, D, V = 3, 6, 2, 4, 128, 50
+    case = Case((64, 640, 128), Hkv=Hkv, D=D, seed=6, spare=0, max_pages=14)  # one free page, two needed
+    case.k.nan_to_num_(0.0)
+    case.v.nan_to_num_(0.0)
+    cache, st = case.gpu(sgd), case.host()
+    nodes, parent = ints([6, 0, 5]), ints([[-1, 0, 0, 1, 2, 2]] * B)
+    grown, ws = sgd.pages_reserve(cache, nodes)
+    assert sgd.workspace_status(ws) == 0x20
+    n = grown - cache.lens
+    cu = torch.nn.functional.pad(n.cumsum(0, dtype=torch.int32), (1, 0))
+    step = cache.with_lens(grown)
+    new = torch.ones(Hkv, 11, D, dtype=torch.bfloat16, device="cuda")
+    assert sgd.workspace_status(sgd.pages_append(step, new, new, cu)) == 0x4  # cu ends at 0, not at 11
+    out, lse, ws = sgd.paged_attn(case.query(M, G).cuda(), G, step, parent, n)
+    assert sgd.workspace_status(ws) == 0 and (out == 0).all() and torch.isneginf(lse).all()
+    u = torch.zeros(B, M, device="cuda")
+    n_path, path, token, ws = sgd.verify_tree(torch.full((B, M, V), 1 / V, device="cuda"), ints([[0] * M] * B), parent, u, u[:, 0].contiguous(),
+                                              n_nodes=n)
+    assert sgd.workspace_status(ws) == 0 and n_path.tolist() == [0] * B and token.tolist() == [-1] * B
+    lens, ws = sgd.pages_accept(step, path, n_path, n)
+    assert sgd.workspace_status(ws) == 0 and lens.tolist() == case.lens.tolist()
+    sgd.pages_release(step, lens)
+    same_state(cache, st)
