@@ -395,9 +395,9 @@ int sgd_decode_attn_noalloc(const void *q, sgd_dtype q_dtype, int G, const sgd_k
  * pages_keep and pages_release branch, cut and end sequences.  All state is in device memory
  * and every call is stream-ordered, so a whole step runs, and is captured, without the host.
  * Where pages_reserve may refuse (NO_PAGES), such a step takes its counts on the device from what was
- * granted: n_nodes[b] = new_lens[b] - lens[b] (new_lens a tensor of its own), cu_new their running sum.  They are 0 after a refusal,
- * and the calls that follow change nothing.  With counts of its own it would take each row's last tokens
- * for the step's: written over by pages_append, dropped by pages_accept.
+ * granted: n_nodes[b] = new_lens[b] - lens[b] (new_lens in memory of its own), cu_new their running sum.
+ * They are 0 after a refusal, and the calls that follow change nothing.  With counts of its own it would
+ * take each row's last tokens for the step's: written over by pages_append, dropped by pages_accept.
  * The pages have no counterpart to these entry points ([CD] names speculative decoding, [NSA]
  * section 2.1 reads the cache by 64-token blocks).
  *
@@ -455,8 +455,9 @@ size_t sgd_paged_workspace_size(const sgd_paged_kv *kv, int G, int M);
  * some query sees must be finite.  A query with a NaN gets NaN, alone.  B * Hkv * (max_pages / 2 + 4)
  * stays below 2^31 (SGD_ERR_SHAPE).
  * Status: BAD_INDEX for a page outside the pool of which a query sees an entry (page 0 is read; the
- * page table entries of other pages may be anything), a parent outside [-1, m) (taken as -1) or n_nodes outside [0, M] (clamped); SIZE_MISMATCH for lens[b] outside
- * [0, 64 * max_pages] (clamped); BAD_SCALE as in sgd_quantize_kv.
+ * page table entries of other pages may be anything), a parent outside [-1, m) (taken as -1) or
+ * n_nodes outside [0, M] (clamped); SIZE_MISMATCH for lens[b] outside [0, 64 * max_pages] (clamped);
+ * BAD_SCALE as in sgd_quantize_kv.
  */
 int sgd_paged_attn(const void *q, int G, int M, const sgd_paged_kv *kv, const int32_t *parent,
                    const int32_t *n_nodes, int window, int sinks, void *out, float *lse, void *workspace,
@@ -509,7 +510,8 @@ int sgd_pages_reserve(const sgd_paged_kv *kv, const int32_t *add, int32_t *new_l
 /*
  * sgd_pages_append -- K and V of new tokens into the pages: of row b the tokens
  * cu_new[b] .. cu_new[b+1] - 1 of k_new and v_new become its last cu_new[b+1] - cu_new[b] entries
- * (lens[b] counts them already, as after a sgd_pages_reserve that was not refused).  An I8 cache takes their codes under
+ * (lens[b] counts them already, as after a sgd_pages_reserve that was not refused).  An I8
+ * cache takes their codes under
  * its scales, as sgd_quantize_kv with SGD_SCHEME_B_CALIBRATED makes them.
  * k_new, v_new   [Hkv, T_new, D] BF16;  cu_new [B+1] int32, T_new = cu_new[B] (host value)
  * Status: BAD_INDEX for a page outside the pool or without references, SHARED_PAGE for one that another row
@@ -567,9 +569,10 @@ int sgd_pages_accept(const sgd_paged_kv *kv, const int32_t *path, const int32_t 
  * idx      [Hkv, kept_total] int32, kept_total >= 1; cu_kept [B+1] int32; new_lens [B] int32, not
  *          lens itself
  * Status: BAD_INDEX and SHARED_PAGE as in sgd_pages_accept (a list that does not ascend or leaves the
- * row; the first token that moves in any head counts for all of them), SIZE_MISMATCH for a row whose range of cu_kept descends, leaves [0, kept_total] or is longer than
- * the row, or whose lens is out of range or more than its held pages (left as it is, new_lens = lens).
- * The pages that fell empty are given back by sgd_pages_release(kv, new_lens, ...).
+ * row; the first token that moves in any head counts for all of them), SIZE_MISMATCH for a row whose
+ * range of cu_kept descends, leaves [0, kept_total] or is longer than the row, or whose lens is out of
+ * range or more than its held pages (left as it is, new_lens = lens).  The pages that fell empty are
+ * given back by sgd_pages_release(kv, new_lens, ...).
  */
 int sgd_pages_keep(const sgd_paged_kv *kv, const int32_t *idx, const int32_t *cu_kept, int64_t kept_total,
                    int32_t *new_lens, void *workspace, size_t workspace_bytes, void *stream);

@@ -268,3 +268,97 @@ def test_a_step_whose_reserve_was_refused_changes_nothing(sgd):
     assert sgd.workspace_status(ws) == 0 and lens.tolist() == case.lens.tolist()
     sgd.pages_release(step, lens)
     same_state(cache, st)
+
+
+def test_int8_attention_is_closer_than_bf16_probabilities(sgd):
+    """On an INT8 cache p enters the second product as float16 with 2^7 (off by at most 2^-11 of itself, or by 2^-32
+    of the largest), where bfloat16 would allow 2^-8: sums that nearly cancel show the difference.
+    Bounds beside the output's 2^-8 |out| and the logits' error as in the other attention tests: Q's bits below 2^-38
+    of its row's maximum are lost; the running sum of L / 16 products of 16 tokens, and 16 of a merge, is rounded (or
+    truncated) to 2^-23 each, twice for the two operands of a sum."""
+    import math
+
+    from oracle import paged as orc
+    lens, G, M, D = (2, 3, 5, 9, 40, 300, 2053), 8, 2, 128
+    case = Case(lens, D=D, dtype="int8", seed=77)
+    case.ks = 0.002  # logits of a few tenths: their own error is far below the bound
+    q = case.query(M, G)
+    out, lse, ws = sgd.paged_attn(q.cuda(), G, case.gpu(sgd))
+    assert sgd.workspace_status(ws) == 0
+    ks, vs = (float(np.float32(x)) for x in (case.ks, case.vs))
+    args = (q.float().numpy(), G, case.k.float().numpy(), case.v.float().numpy(), case.table, case.lens, None, None, 0, 0, ks, vs)
+    ref, rlse, mass, zabs = orc.attn(*args)
+    L = np.array(lens, float)[:, None, None, None]
+    qmax = np.abs(q.float().numpy()).max(-1)[..., None]
+    tz = 2.0 ** -15.9 * zabs[..., None] + 2.0 ** -18 + 2.0 ** -38 * qmax * 127 * ks * math.sqrt(D)
+    tol = (2.0 ** -11 + 2 * tz + 2.0 ** -22 * (L / 16 + 16)) * mass + L * 2.0 ** -32 * 127 * vs + 2.0 ** -8 * np.abs(ref)
+    assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
+    # the same bound finds probabilities that were rounded to bfloat16
+    off = 0
+    for b, n in enumerate(lens):
+        for h in range(2):
+            kk, vv = orc.rows(args[2], case.table[b], n, h) * ks, orc.rows(args[3], case.table[b], n, h) * vs
+            for m in range(M):
+                see = n - M + m + 1
+                z = kk[:see] @ args[0][b, m, h * G:h * G + G].astype(np.float64).T / math.sqrt(D)
+                e = np.exp(z - z.max(0))
+                p = torch.from_numpy(e).bfloat16().double().numpy() / e.sum(0)
+                here = slice(h * G, h * G + G)
+                off += (np.abs(p.T @ vv[:see] - ref[b, m, here]) > tol[b, m, here]).sum()
+    assert off > 20
+
+
+@pytest.mark.parametrize("D,Hkv", [(64, 3), (128, 1)])
+def test_append_codes_at_other_sizes(sgd, D, Hkv):
+    import oracle
+    rng = np.random.default_rng(D)
+    new = [33, 0, 130, 1]
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    case = Case((70, 3, 200, 64), Hkv=Hkv, D=D, dtype="int8", seed=D)
+    cache, st = case.gpu(sgd), case.host()
+    k, v = (torch.from_numpy(rng.standard_normal((Hkv, cu[-1], D), dtype=np.float32) * np.float32(1.5)).bfloat16() for _ in range(2))
+    assert sgd.workspace_status(sgd.pages_append(cache, k.cuda(), v.cuda(), ints(cu))) == 0
+    codes = [oracle.quantize(x.float().numpy(), np.float32(s)) for x, s in ((k, case.ks), (v, case.vs))]
+    st.append(codes[0].reshape(k.shape), codes[1].reshape(v.shape), cu)
+    same_state(cache, st)
+
+
+def test_calls_from_two_host_threads(sgd):
+    """Each thread with a stream, a cache and workspaces of its own, the same kernels at the same time."""
+    import threading
+    cases = [Case([int(x) for x in np.random.default_rng(s).integers(10, 3000, 6)], seed=s, spare=40, max_pages=60) for s in (3, 4)]
+    qs = [c.query(5, 8).cuda() for c in cases]
+    add = ints([5] * 6)
+
+    def work(i, stream):
+        cache = cases[i].gpu(sgd)
+        torch.cuda.synchronize()
+        done = []
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                out, lse, ws = sgd.paged_attn(qs[i], 8, cache)
+                new, ws2 = sgd.pages_reserve(cache, add)
+                ws3 = sgd.pages_release(cache, cache.lens)
+                done.append((out, lse, new, ws, ws2, ws3))
+        stream.synchronize()
+        return done
+
+    want = [work(i, torch.cuda.Stream())[0] for i in (0, 1)]
+    got, failed = [None, None], []
+
+    def thread(i):
+        try:
+            got[i] = work(i, torch.cuda.Stream())
+        except BaseException as e:  # noqa: BLE001  (reported by the test, not lost with the thread)
+            failed.append(e)
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for i in (0, 1):
+        for out, lse, new, *ws in got[i]:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1]) and torch.equal(new, want[i][2])
+            assert all(sgd.workspace_status(w) == 0 for w in ws)
