@@ -510,9 +510,8 @@ int sgd_pages_reserve(const sgd_paged_kv *kv, const int32_t *add, int32_t *new_l
 /*
  * sgd_pages_append -- K and V of new tokens into the pages: of row b the tokens
  * cu_new[b] .. cu_new[b+1] - 1 of k_new and v_new become its last cu_new[b+1] - cu_new[b] entries
- * (lens[b] counts them already, as after a sgd_pages_reserve that was not refused).  An I8
- * cache takes their codes under
- * its scales, as sgd_quantize_kv with SGD_SCHEME_B_CALIBRATED makes them.
+ * (lens[b] counts them already, as after a sgd_pages_reserve that was not refused).  An I8 cache takes
+ * their codes under its scales, as sgd_quantize_kv with SGD_SCHEME_B_CALIBRATED makes them.
  * k_new, v_new   [Hkv, T_new, D] BF16;  cu_new [B+1] int32, T_new = cu_new[B] (host value)
  * Status: BAD_INDEX for a page outside the pool or without references, SHARED_PAGE for one that another row
  * holds too, SIZE_MISMATCH for a token outside the row and its held pages or a cu_new that disagrees with T_new

@@ -49,7 +49,6 @@ struct Shared {
     int32_t gone[SGD_MAX_NODES];                  // chosen drafts refused at this node (q == NULL)
     double part[2][kVerifyCluster];               // every CTA's part of the sum, of this and the last one
     double wsum[kVerifyWarps];                    // this CTA's warps' parts
-    int32_t found;
 };
 
 // N consecutive values, one load where N > 1
@@ -92,7 +91,6 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(VerifyArgs a,
         }
     }
     if (rank == 0 && bad) atomicOr(a.status, bad);
-    if (tid == 0) sh.found = -1;
     cluster.sync();  // the shared arrays, and every CTA of the cluster is there
     if (n == 0) {
         if (rank == 0) {
