@@ -52,8 +52,9 @@ namespace sgd {
 namespace {
 
 constexpr int kTile = 128;       // tokens of a KV tile, rows of a row tile
-// tiles of work charged to an item beside its own (start, epilogue): 64 users' windows of 4096 tokens take 134, 128, 129,
-// 131 us with 2, 3, 4, 6
+// Tiles of work charged to an item beside its own (start, epilogue).  With 1, 2, 3, 4, 6, cold L2: 64 windows of 4096 tokens
+// 160, 146, 144, 142, 147 us; 64 INT8 rows of 200 to 8000 tokens 92, 84, 73, 71, 77; 256 rows of 100 to 2000 74, 59, 57, 56, 59;
+// 16 rows of 300 to 9000, 16 nodes, 52, 50, 46, 46, 46; 128 rows of 1000 114, whatever the charge
 constexpr int kItemCharge = 3;
 constexpr float kSlack = 8.f;    // log2 by which the true maximum may pass the reference
 constexpr int kWarpProducer = 0, kWarpMma = 1, kWarpSoftmax = 4, kWarpConvert = 12;  // softmax: 4..11
@@ -1043,10 +1044,12 @@ int launch(const PagedView &kv, const PagedAttnArgs &a, const AttnPlan &plan, cu
     const cudaError_t e =
         launch_k_early(kern, dim3(plan.n_ranges * plan.RT), dim3(C::THREADS), C::SMEM, s, kv, a, plan, mq, mk, mv);
     if (e != cudaSuccess) return SGD_ERR_CUDA;
-    // few rows may have many ranges each (up to all of them): then a CTA per row; many rows have few
+    // Few rows may have many ranges each (up to all of them): then a CTA per row, else a warp.  Whole call, CTA against warp
+    // per row, cold L2: 64 rows of 128K tokens 103 and 106 us, 512 rows of 16K 29.7 and 31.7; 1024 rows of 512 to 32K 105 and
+    // 103, 2048 INT8 rows of 16K to 32K 140 and 136, 4096 rows of 1K to 16K 58 and 50
     const int64_t n_rows = (int64_t)kv.B * a.M * kv.Hkv * a.G;
     constexpr int W = kMergeThreads / 32;
-    if (n_rows <= 2048)
+    if (n_rows <= 512)
         launch_k_early(paged_merge_kernel<C::D, W>, dim3((unsigned)n_rows), dim3(kMergeThreads), 0, s, kv, a, plan, (int)C::TWO, n_rows);
     else
         launch_k_early(paged_merge_kernel<C::D, 1>, dim3((unsigned)((n_rows + W - 1) / W)), dim3(kMergeThreads), 0, s, kv, a, plan,
