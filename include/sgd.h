@@ -451,6 +451,9 @@ size_t sgd_paged_workspace_size(const sgd_paged_kv *kv, int G, int M);
  * parent   [B, M] int32 or NULL; n_nodes [B] int32 or NULL
  * window   >= 0, 0 = unlimited; sinks >= 0, read with a window only
  * out      [B, M, Hq, D] BF16; lse [B, M, Hq] float32, natural log
+ * The logits, their maximum and sums and the accumulated products are float32.  The probabilities enter the
+ * second product as bfloat16 on a BF16 cache (each off by at most 2^-8 of itself, out by 2^-8 sum p |v|), as
+ * float16 on an I8 cache (2^-11, or 2^-32 of the largest).
  * K and V of an entry that no query of the sequence sees may be anything; those of an entry that
  * some query sees must be finite.  A query with a NaN gets NaN, alone.  B * Hkv * (max_pages / 2 + 4)
  * stays below 2^31 (SGD_ERR_SHAPE).
@@ -474,7 +477,9 @@ int sgd_paged_attn(const void *q, int G, int M, const sgd_paged_kv *kv, const in
  *   they were where that sum is not positive).  q == NULL: the drafts were not drawn but chosen;
  *   q(x) is 1 in the test and a refused token's w(x) becomes 0.  Where no child is left the next
  *   token is drawn from w: the lowest x with w(0) + .. + w(x) > u_sample[b] * sum w.
- *   Products, sums and residuals are formed in 64 bits.
+ *   Products, sums and residuals are formed in 64 bits; after several refusals at a node w is off by up to
+ *   2^-52 of p over the product of the node's Z, which matters below a product of about 2^-40 (drafted
+ *   tokens of that draft probability) alone.
  * p, q     [B, M, V], F32 or BF16 (p_dtype, for both)
  * tokens   [B, M] int32 (node 0's is not read); parent [B, M] int32; n_nodes [B] int32 or NULL
  * u_accept [B, M] float32; u_sample [B] float32, in [0, 1)

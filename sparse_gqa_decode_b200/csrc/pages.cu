@@ -324,7 +324,9 @@ __global__ void __launch_bounds__(256) append_kernel(PagedView kv, const __nv_bf
 // entry overwrote), so the steps' sources stream through a ring of asynchronous copies, two steps of 32 KB
 // ahead, and their list entries as far ahead of those.  A step has a row for every thread, which finds where it
 // comes from and goes to; with fewer rows a step, or pieces looked up one by one, the lookups bound the kernel
-// (8 x 32K tokens kept to an eighth: 94 us piece by piece, 79 us with 64 rows a step, 51 us with 256).
+// (8 x 32K tokens kept to an eighth: 94 us piece by piece, 79 us with 64 rows a step, 52 us with 256).  What is left:
+// page table entries looked up in global memory between a step's two barriers (long scoreboard 3.1 warps an issue, short 1.8,
+// DRAM 28%), and unequal CTAs (active cycles of an SM 18 to 43 thousand).
 // CTA (row, KV head; K or V; slice of the row's bytes); LANES threads of 16 bytes to a slice.
 constexpr int kCompactThreads = 256, kRing = 3;
 
